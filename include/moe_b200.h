@@ -94,9 +94,31 @@ typedef int moe_status_t;
  * and MXFP8 keeps the stage-2 operand h at 8 bits. */
 #define MOE_DT_MXFP4_E2M1 5
 
+/* No quantised output (moe_rmsnorm_quantize). */
+#define MOE_DT_NONE (-1)
+
 /* Routing modes of moe_router_topk. */
 #define MOE_ROUTE_SOFTMAX 0
 #define MOE_ROUTE_GROUPED_SIGMOID 1
+
+/* Scores and group scores of moe_route. */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_GROUP_TOP2 0 /* sum of the group's two largest choice values */
+#define MOE_GROUP_MAX 1  /* its largest */
+
+/* Expert id of a padding row of a batch (moe_route): moe_align_sort drops its
+ * slots without an error, moe_append_shared_slots gives the row no shared
+ * slots, and stage 2 leaves the row of the output as it was. */
+#define MOE_NO_EXPERT INT32_MIN
+
+/* Activations of moe_linear. */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_RELU 1
+#define MOE_ACT_SILU 2
+#define MOE_ACT_GELU 3      /* v * Phi(v) */
+#define MOE_ACT_GELU_TANH 4 /* 0.5 v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) */
+#define MOE_ACT_SIGMOID 5
 
 /* Largest sizes the kernels cover. */
 #define MOE_MAX_EXPERTS 512
@@ -246,7 +268,8 @@ moe_status_t moe_router_gemm_topk(int dtype, const void* x, const void* w_r, con
  *   expert_counts int32 [E]; expert_offsets int32 [E+1] (padded prefix sum);
  *   num_padded    int32 [1] = expert_offsets[E].
  * Checks: block_m in {16,32,64,128,256}; T*k <= 1<<20; E <= MOE_MAX_EXPERTS.
- * An expert id outside [0,E) sets device error 2 and is dropped.
+ * An expert id outside [0,E) sets device error 2 and is dropped
+ * (MOE_NO_EXPERT: dropped without an error).
  * One CTA of 1024 threads below 4096 slots; from 4096 on, a cluster of 8 such
  * CTAs, each sorting its eighth of the slots and reading the others' per-expert
  * counts over distributed shared memory (the results are the same). */
@@ -265,7 +288,8 @@ moe_status_t moe_align_sort(const int32_t* topk_ids, int T, int top_k, int E, in
  * moe_align_sort (E + m experts, k + m slots) and the two grouped GEMMs then
  * compute routed and shared experts in the same launches, and stage 2 sums
  * all k + m contributions before its one rounding (no addend, no side
- * stream). Checks: E + m <= MOE_MAX_EXPERTS, k + m <= MOE_MAX_TOPK. */
+ * stream). A row whose first id is MOE_NO_EXPERT gets MOE_NO_EXPERT with
+ * weight 0 in its shared slots too. Checks: E + m <= MOE_MAX_EXPERTS, k + m <= MOE_MAX_TOPK. */
 moe_status_t moe_append_shared_slots(const int32_t* topk_ids, const float* topk_weights, int T, int top_k,
                                      int E, int m, const void* gate, int gate_dtype, int32_t* out_ids,
                                      float* out_weights, moe_stream_t stream);
@@ -415,6 +439,100 @@ moe_status_t moe_stage2_gemm_accumulate_static_ws(int dtype, const void* h, cons
  *   x [T,K], w [K], out [T]. Checks: T >= 1, K >= 1. */
 moe_status_t shared_expert_gate_dot(int dtype, const void* x, const void* w, int T, int K,
                                     int apply_sigmoid, void* out, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Operators around the layer: the dense products, the norm and the general
+ * routing that a decoder block runs next to its expert layer. */
+
+/* moe_linear: dense matrix product with everything that follows it in its
+ * epilogue:
+ *     y[t,n] = act( (sum_k x[t,k] * w[n,k]) * x_scale[t] * w_scale[n] + bias[n] )
+ *     out[t,n] = round( y[t,n] + residual[t,n] )
+ * fp32 accumulation and epilogue, one rounding to the output type. Serves the
+ * attention output projection onto the residual stream, router logits in fp32
+ * and dense feed-forward projections, from one token to a whole prefill.
+ *   dtype      type of x and w: MOE_DT_BF16, MOE_DT_FP16 or MOE_DT_FP8_E4M3.
+ *   x          [T,K], rows ldx elements apart; w [N,K], rows ldw apart (K
+ *              contiguous in both).
+ *   x_scale    fp32 [T] and w_scale fp32 [w_scale_rows], w_scale_rows = N (one
+ *              per output) or 1 (one per matrix): FP8 only, NULL otherwise.
+ *   bias       [N] of bias_dtype (BF16, FP16, F32), or NULL.
+ *   act        MOE_ACT_*, evaluated in fp32 with the fast exponential
+ *              (relative error near 2^-21); NaN and infinities follow the
+ *              formula.
+ *   residual   [T,N] of out_dtype, rows ldr apart, or NULL. It may be out
+ *              itself (same address and stride); any other overlap of out
+ *              with an operand is undefined.
+ *   out        [T,N] of out_dtype (BF16, FP16, F32), rows ldo apart; nothing
+ *              between the rows is written.
+ * No workspace; results do not depend on the launch (a K split is added in a
+ * fixed order), but sums of different T, N or K may be ordered differently.
+ * Checks: T >= 0 (T == 0: nothing is launched), N, K >= 1, ldx, ldw >= K,
+ * ldo, ldr >= N; x and w 16-byte aligned with row strides of a multiple of 16
+ * bytes (MOE_ERR_ALIGNMENT), out, residual, bias and the scales aligned to
+ * their own type. Asynchronous on `stream`, a stream of the current device. */
+moe_status_t moe_linear(int dtype, const void* x, int64_t ldx, const float* x_scale, const void* w,
+                        int64_t ldw, const float* w_scale, int w_scale_rows, const void* bias,
+                        int bias_dtype, int act, const void* residual, int64_t ldr, void* out,
+                        int out_dtype, int64_t ldo, int T, int N, int K, moe_stream_t stream);
+
+/* moe_route: routing of T tokens over E experts in its general form.
+ *     s = softmax(l) over the live experts, or sigmoid(l); in double,
+ *     c = fp32(s) + bias                      (what the choice goes by)
+ *     group score = sum of the two largest c of the group's live experts (one
+ *         if only one lives), or the largest; the topk_group best groups are
+ *         kept (ties: lower group)
+ *     the top_k largest c of the kept groups are picked (ties: lower index)
+ *     w_j = s_j / sum of the picked s (renormalize != 0), or s_j; times
+ *         routed_scaling_factor; rounded once.
+ *   logits       [T,E] of logits_dtype (F32, BF16, FP16), rows ld apart.
+ *   bias         fp32 [E] balance bias or NULL; it moves the choice, never a
+ *                weight.
+ *   expert_mask  uint8 [E], 0 = switched off, or NULL.
+ *   num_valid    int32 [1] on the device or NULL: rows t >= *num_valid are
+ *                padding and get MOE_NO_EXPERT with weight 0.
+ *   An expert is dead for a token when it is switched off, its logit is NaN or
+ *   -inf, or its c is NaN or -inf. Dead experts of the kept groups are picked
+ *   after all live ones, lowest index first, with weight 0; a row without a
+ *   live expert gets weights 0. Logits of +inf share a softmax evenly.
+ *   topk_ids     int32 [T,top_k], best first; topk_weights fp32 [T,top_k].
+ * Against moe_router_topk: a bias, groups and either score in any combination,
+ * 16-bit and strided logits, masks and padded batches; softmax is chosen by
+ * the rounded probability rather than by the logit.
+ * Checks: T >= 0 (T == 0: nothing is launched), 1 <= E <= MOE_MAX_EXPERTS,
+ * 1 <= top_k <= min(E, MOE_MAX_TOPK), n_group divides E, 1 <= topk_group <=
+ * n_group <= 32, top_k <= topk_group * E / n_group, ld >= E. Asynchronous on
+ * `stream`. */
+moe_status_t moe_route(const void* logits, int logits_dtype, int64_t ld, const float* bias,
+                       const uint8_t* expert_mask, const int32_t* num_valid, int T, int E, int top_k,
+                       int score, int n_group, int topk_group, int group_score, int renormalize,
+                       float routed_scaling_factor, int32_t* topk_ids, float* topk_weights,
+                       moe_stream_t stream);
+
+/* moe_rmsnorm_quantize: residual add, RMS norm and quantisation in one pass.
+ *     z = x + residual (fp32),  residual_out = round(z)
+ *     y = z * rsqrt(mean_h(z^2) + eps) * gamma (fp32, from the unrounded z)
+ * y is stored rounded once to x's type, quantised (from the unrounded y) to a
+ * stage-1 operand format, or both: the 16-bit rows feed the router and the
+ * shared gate, the codes the expert GEMMs.
+ *   dtype      type of x, residual, residual_out and y: MOE_DT_BF16 or
+ *              MOE_DT_FP16, all [T,H] dense.
+ *   quant      MOE_DT_NONE (codes and scale NULL), MOE_DT_FP8_E4M3 or
+ *              MOE_DT_MXFP8_E4M3: codes [T,H] and scale as in
+ *              moe_quantize_activations (the amax of a row or block is taken
+ *              over its non-NaN values; a NaN gets the NaN code).
+ *   residual   or NULL (z = x). residual_out or NULL; it may be residual or x
+ *              itself, and y may be x itself.
+ *   gamma      [H] of gamma_dtype: dtype or F32.
+ * The sum of squares is taken in fp32: a row whose sum passes the fp32 range
+ * gives zeros.
+ * Checks: T >= 0 (T == 0: nothing is launched), eps > 0, H % 8 == 0 (MXFP8:
+ * % 32), H <= 16384, x, residual, gamma, residual_out and y 16-byte aligned,
+ * codes 8-byte aligned; at least one output. Asynchronous on `stream`. */
+moe_status_t moe_rmsnorm_quantize(int dtype, int quant, const void* x, const void* residual,
+                                  const void* gamma, int gamma_dtype, float eps, int T, int H,
+                                  void* residual_out, void* y, void* codes, void* scale,
+                                  moe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -21,10 +21,17 @@ MX_FORMATS = ("mxfp8", "mxfp4")
 DTYPES = {"bf16": MOE_DT_BF16, "fp16": MOE_DT_FP16, "fp8": MOE_DT_FP8_E4M3, "mxfp8": MOE_DT_MXFP8_E4M3,
           "mxfp4": MOE_DT_MXFP4_E2M1,
           "f32": MOE_DT_F32}
+MOE_DT_NONE = -1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_TOP2, MOE_GROUP_MAX = 0, 1
+MOE_NO_EXPERT = -(1 << 31)  # expert id of a padding row
+SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+GROUP_SCORES = {"top2": MOE_GROUP_TOP2, "max": MOE_GROUP_MAX}
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "sigmoid": 5}
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_b200.so")
 
 # name -> (restype, argtypes)
-_P, _I, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_P, _I, _F, _SZ, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_int64
 SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [_I]),
     "moe_version": (ctypes.c_char_p, []),
@@ -48,6 +55,9 @@ SIGNATURES = {
                                                   _P, _P, _P, _P]),
     "shared_expert_gate_dot": (_I, [_I, _P, _P, _I, _I, _I, _P, _P]),
     "moe_quantize_activations": (_I, [_I, _P, _I, _I, _P, _P, _P]),
+    "moe_linear": (_I, [_I, _P, _L, _P, _P, _L, _P, _I, _P, _I, _I, _P, _L, _P, _I, _L, _I, _I, _I, _P]),
+    "moe_route": (_I, [_P, _I, _L, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P]),
+    "moe_rmsnorm_quantize": (_I, [_I, _I, _P, _P, _P, _I, _F, _I, _I, _P, _P, _P, _P, _P]),
     "moe_append_shared_slots": (_I, [_P, _P, _I, _I, _I, _I, _P, _I, _P, _P, _P]),
 }
 
@@ -214,3 +224,104 @@ def shared_expert_gate_dot(dtype, x, w, apply_sigmoid, out, stream=None):
     T, K = x.shape
     _check("shared_expert_gate_dot", lib().shared_expert_gate_dot(
         dtype, _ptr(x), _ptr(w), T, K, int(apply_sigmoid), _ptr(out), _stream(stream)))
+
+
+_FLOAT_DT = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_FP16, torch.float32: MOE_DT_F32}
+_OPERAND_DT = {MOE_DT_BF16: (torch.bfloat16,), MOE_DT_FP16: (torch.float16,),
+               MOE_DT_FP8_E4M3: (torch.uint8, torch.float8_e4m3fn)}
+
+
+def _rows(t, name, shape, types):
+    """(address, row stride in elements) of a 2-D tensor whose rows are dense."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.dtype not in types:
+        raise TypeError(f"{name} has type {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    rows, cols = shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    ld = t.stride(0)
+    return t.data_ptr(), ld if rows > 1 and ld >= cols else _dense_ld(name, t, rows, cols)
+
+
+def _dense_ld(name, t, rows, cols):
+    """Row stride of a tensor with one row or none, whose own says nothing; an
+    expanded or overlapping tensor is refused."""
+    if rows > 1:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return -(-cols // 16) * 16
+
+
+def _vec(t, name, n, types):
+    if t is None:
+        return None
+    if t.dtype not in types:
+        raise TypeError(f"{name} has type {t.dtype}")
+    if t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
+    return _ptr(t)
+
+
+def _same_device(first, *others):
+    """The calls launch on the current device's stream: every tensor lives there."""
+    dev = first.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {dev}, current device {torch.cuda.current_device()}")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+
+
+def moe_linear(dtype, x, x_scale, w, w_scale, bias, act, residual, out, stream=None):
+    """out = act((x . w^T) * x_scale * w_scale + bias) + residual; x [T,K], w
+    [N,K], residual and out [T,N] may be views with any row stride."""
+    T, K = x.shape
+    N = w.shape[0]
+    if dtype not in _OPERAND_DT:
+        raise MoEError("moe_linear", -2)
+    ops = _OPERAND_DT[dtype]
+    px, ldx = _rows(x, "x", (T, K), ops)
+    pw, ldw = _rows(w, "w", (N, K), ops)
+    po, ldo = _rows(out, "out", (T, N), _FLOAT_DT)
+    pr, ldr = (None, 0) if residual is None else _rows(residual, "residual", (T, N), (out.dtype,))
+    f32 = (torch.float32,)
+    ws_rows = 1 if w_scale is None else w_scale.numel()
+    _same_device(x, w, out, residual, bias, x_scale, w_scale)
+    _check("moe_linear", lib().moe_linear(
+        dtype, px, ldx, _vec(x_scale, "x_scale", T, f32), pw, ldw, _vec(w_scale, "w_scale", ws_rows, f32), ws_rows,
+        _vec(bias, "bias", N, _FLOAT_DT), MOE_DT_F32 if bias is None else _FLOAT_DT[bias.dtype], act, pr, ldr, po,
+        _FLOAT_DT[out.dtype], ldo, T, N, K, _stream(stream)))
+
+
+def moe_route(logits, bias, expert_mask, num_valid, top_k, score, n_group, topk_group, group_score, renormalize,
+              routed_scaling_factor, topk_ids, topk_weights, stream=None):
+    """Routing from softmax or sigmoid scores; logits [T,E] may be a view with
+    any row stride."""
+    T, E = logits.shape
+    pl, ld = _rows(logits, "logits", (T, E), _FLOAT_DT)
+    _same_device(logits, bias, expert_mask, num_valid, topk_ids, topk_weights)
+    _check("moe_route", lib().moe_route(
+        pl, _FLOAT_DT[logits.dtype], ld, _vec(bias, "bias", E, (torch.float32,)),
+        _vec(expert_mask, "expert_mask", E, (torch.uint8, torch.bool)),
+        _vec(num_valid, "num_valid", 1, (torch.int32,)), T, E, top_k, score, n_group, topk_group, group_score,
+        int(renormalize), float(routed_scaling_factor), _vec(topk_ids, "topk_ids", T * top_k, (torch.int32,)),
+        _vec(topk_weights, "topk_weights", T * top_k, (torch.float32,)), _stream(stream)))
+
+
+def moe_rmsnorm_quantize(quant, x, residual, gamma, eps, residual_out, y, codes, scale, stream=None):
+    """z = x + residual -> residual_out; RMS norm of z -> y and / or codes with
+    scale. ``quant``: MOE_DT_FP8_E4M3, MOE_DT_MXFP8_E4M3, or None."""
+    T, H = x.shape
+    same = (x.dtype,)
+    dtype = _FLOAT_DT.get(x.dtype, MOE_DT_F32)
+    q = MOE_DT_NONE if quant is None else quant
+    mx = q == MOE_DT_MXFP8_E4M3
+    _same_device(x, residual, gamma, residual_out, y, codes, scale)
+    _check("moe_rmsnorm_quantize", lib().moe_rmsnorm_quantize(
+        dtype, q, _ptr(x), _vec(residual, "residual", T * H, same),
+        _vec(gamma, "gamma", H, (x.dtype, torch.float32)), _FLOAT_DT[gamma.dtype], float(eps), T, H,
+        _vec(residual_out, "residual_out", T * H, same), _vec(y, "y", T * H, same),
+        _vec(codes, "codes", T * H, (torch.uint8, torch.float8_e4m3fn)),
+        _vec(scale, "scale", T * H // 32 if mx else T, (torch.uint8,) if mx else (torch.float32,)), _stream(stream)))

@@ -13,8 +13,11 @@
 #include "moe_b200.h"
 #include "gate.cuh"
 #include "gemm.cuh"
+#include "linear.cuh"
+#include "norm.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
+#include "route.cuh"
 #include "router.cuh"
 #include "selftest.cuh"
 #include "sort.cuh"
@@ -399,6 +402,122 @@ moe_status_t launch_router_gemm_vpl(const moe::RouterGemmArgs& a, cudaStream_t s
   if (vpl <= 4) return wide ? launch_router_gemm<4, 16, TX>(a, s) : launch_router_gemm<4, 4, TX>(a, s);
   if (vpl <= 8) return wide ? launch_router_gemm<8, 16, TX>(a, s) : launch_router_gemm<8, 4, TX>(a, s);
   return launch_router_gemm<16, 4, TX>(a, s);
+}
+
+// ------------------------------------------------------------ linear, route, norm dispatch
+
+inline bool is_16bit(int dtype) { return dtype == MOE_DT_BF16 || dtype == MOE_DT_FP16; }
+inline bool is_float_dt(int dtype) { return is_16bit(dtype) || dtype == MOE_DT_F32; }
+inline int float_size(int dtype) { return dtype == MOE_DT_F32 ? 4 : 2; }
+inline bool aligned_to(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// 2D operand of the linear product: `rows` rows of K elements, ld elements
+// apart, read in boxes of one 128-byte K atom x box_rows.
+moe_status_t make_linear_map(CUtensorMap* m, int dtype, const void* base, int rows, int K, int64_t ld, int box_rows) {
+  const int es = is_16bit(dtype) ? 2 : 1;
+  const CUtensorMapDataType dt = dtype == MOE_DT_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                 : dtype == MOE_DT_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t st[1] = {static_cast<cuuint64_t>(ld) * es};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(moe::kTileKBytes / es), static_cast<cuuint32_t>(box_rows)};
+  return make_map(m, dt, 2, base, dims, st, box);
+}
+
+struct LinearCall {
+  int dtype;
+  const void *x, *w;
+  int64_t ldx, ldw;
+  int K;
+  moe::LinearArgs g;
+};
+
+template <int BN, bool FP8>
+moe_status_t launch_linear_split(const LinearCall& c, int S, cudaStream_t s) {
+  using L = moe::SplitCfg<BN>;
+  static_assert(L::kBytes <= 227 * 1024, "shared memory per CTA");
+  CUtensorMap tw, tx;
+  moe_status_t r = make_linear_map(&tw, c.dtype, c.w, c.g.N, c.K, c.ldw, moe::kTileM);
+  if (r != MOE_OK) return r;
+  r = make_linear_map(&tx, c.dtype, c.x, c.g.T, c.K, c.ldx, BN);
+  if (r != MOE_OK) return r;
+  auto kern = moe::k_linear_split<BN, FP8>;
+  static std::atomic<int> attr_set[64];
+  r = set_smem_attr(kern, L::kBytes, attr_set);
+  if (r != MOE_OK) return r;
+  moe::LinearArgs g = c.g;
+  g.n_tb = (g.T + BN - 1) / BN;
+  const int64_t ctas = static_cast<int64_t>((g.N + moe::kTileM - 1) / moe::kTileM) * g.n_tb * S;
+  if (ctas > INT32_MAX) return MOE_ERR_SHAPE;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = static_cast<unsigned>(S);
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(moe::kSplitThreads);
+  cfg.dynamicSmemBytes = L::kBytes;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  MOE_CK(cudaLaunchKernelEx(&cfg, kern, tw, tx, g, S));
+  return MOE_OK;
+}
+
+template <bool FP8>
+moe_status_t launch_linear(const LinearCall& c, cudaStream_t s) {
+  const int bn = c.g.T <= 16 ? 16 : c.g.T <= 32 ? 32 : c.g.T <= 64 ? 64 : c.g.T <= 128 ? 128 : 256;
+  const int64_t tiles = static_cast<int64_t>((c.g.N + 127) / 128) * ((c.g.T + bn - 1) / bn);
+  int S = 8;
+  while (S > 1 && (tiles * S > num_sms() || c.g.nk < 4 * S)) S /= 2;
+  switch (bn) {
+    case 16: return launch_linear_split<16, FP8>(c, S, s);
+    case 32: return launch_linear_split<32, FP8>(c, S, s);
+    case 64: return launch_linear_split<64, FP8>(c, S, s);
+    case 128: return launch_linear_split<128, FP8>(c, S, s);
+  }
+  return launch_linear_split<256, FP8>(c, S, s);
+}
+
+template <int VPL>
+moe_status_t launch_route(const moe::RouteArgs& a, bool softmax, cudaStream_t s) {
+  const moe::RouteGroups G(a.E, a.n_group);
+  const size_t smem = a.n_group > 1 ? moe::kRouteWarps * G.smem_words(a.n_group) * sizeof(float) : 0;
+  const int blocks = (a.T + moe::kRouteWarps - 1) / moe::kRouteWarps;
+  if (softmax) moe::k_route<VPL, true><<<blocks, moe::kRouteWarps * 32, smem, s>>>(a);
+  else moe::k_route<VPL, false><<<blocks, moe::kRouteWarps * 32, smem, s>>>(a);
+  MOE_CK(cudaGetLastError());
+  return MOE_OK;
+}
+
+template <typename TX, int Q, int TPR, int V>
+moe_status_t launch_rmsnorm(const moe::NormArgs& a, cudaStream_t s) {
+  constexpr int threads = TPR > 256 ? TPR : 256;
+  constexpr int rows = threads / TPR;
+  moe::k_rmsnorm<TX, Q, TPR, V><<<(a.T - 1) / rows + 1, threads, 0, s>>>(a);
+  MOE_CK(cudaGetLastError());
+  return MOE_OK;
+}
+
+// Threads per row and 16-byte chunks per thread, by the row's chunk count.
+template <typename TX, int Q>
+moe_status_t launch_rmsnorm_row(const moe::NormArgs& a, cudaStream_t s) {
+  const int nc = a.H / 8;
+  if (nc <= 32) return launch_rmsnorm<TX, Q, 32, 1>(a, s);
+  if (nc <= 64) return launch_rmsnorm<TX, Q, 64, 1>(a, s);
+  if (nc <= 128) return launch_rmsnorm<TX, Q, 128, 1>(a, s);
+  if (nc <= 256) return launch_rmsnorm<TX, Q, 256, 1>(a, s);
+  if (nc <= 512) return launch_rmsnorm<TX, Q, 512, 1>(a, s);
+  if (nc <= 1024) return launch_rmsnorm<TX, Q, 512, 2>(a, s);
+  return launch_rmsnorm<TX, Q, 512, 4>(a, s);
+}
+
+template <typename TX>
+moe_status_t launch_rmsnorm_quant(const moe::NormArgs& a, int q, cudaStream_t s) {
+  if (q == moe::kNormFp8) return launch_rmsnorm_row<TX, moe::kNormFp8>(a, s);
+  if (q == moe::kNormMx) return launch_rmsnorm_row<TX, moe::kNormMx>(a, s);
+  return launch_rmsnorm_row<TX, moe::kNormPlain>(a, s);
 }
 
 // Argument checks of stage 2, shared by moe_stage2_gemm_accumulate and
@@ -896,6 +1015,115 @@ moe_status_t moe_stage2_gemm_accumulate_static_ws(int dtype, const void* h, cons
   return moe_stage2_gemm_accumulate(dtype, h, h_scale, w2, w2_scale, weights, weights_dtype, sorted_ids,
                                     block_expert, num_padded, T, top_k, H, I, E, block_m, addend, addend_ready, ws,
                                     out, stream);
+}
+
+moe_status_t moe_linear(int dtype, const void* x, int64_t ldx, const float* x_scale, const void* w, int64_t ldw,
+                        const float* w_scale, int w_scale_rows, const void* bias, int bias_dtype, int act,
+                        const void* residual, int64_t ldr, void* out, int out_dtype, int64_t ldo, int T, int N, int K,
+                        moe_stream_t stream) {
+  const bool fp8 = dtype == MOE_DT_FP8_E4M3;
+  if (!is_16bit(dtype) && !fp8) return MOE_ERR_UNSUPPORTED_DTYPE;
+  if (!is_float_dt(out_dtype) || (bias && !is_float_dt(bias_dtype))) return MOE_ERR_UNSUPPORTED_DTYPE;
+  if (T < 0 || N < 1 || K < 1 || act < MOE_ACT_NONE || act > MOE_ACT_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || !w || !out) return MOE_ERR_INVALID_ARG;
+  if (fp8 ? (!x_scale || !w_scale || (w_scale_rows != 1 && w_scale_rows != N)) : (x_scale || w_scale))
+    return MOE_ERR_INVALID_ARG;
+  if (ldx < K || ldw < K || ldo < N || (residual && ldr < N)) return MOE_ERR_INVALID_ARG;
+  const int es = fp8 ? 1 : 2;
+  const int64_t row_max = int64_t{1} << 36;  // row strides the tensor maps and 64-bit offsets cover
+  if (ldx > row_max || ldw > row_max || ldo > row_max || (residual && ldr > row_max)) return MOE_ERR_SHAPE;
+  const int os = float_size(out_dtype);
+  if (!aligned16(x) || !aligned16(w) || ldx * es % 16 != 0 || ldw * es % 16 != 0 || !aligned_to(out, os) ||
+      (residual && !aligned_to(residual, os)) || (bias && !aligned_to(bias, float_size(bias_dtype))) ||
+      !aligned_to(x_scale, 4) || !aligned_to(w_scale, 4))
+    return MOE_ERR_ALIGNMENT;
+  LinearCall c{};
+  c.dtype = dtype;
+  c.x = x;
+  c.w = w;
+  c.ldx = ldx;
+  c.ldw = ldw;
+  c.K = K;
+  moe::LinearArgs& g = c.g;
+  g.T = T;
+  g.N = N;
+  g.nk = static_cast<int>((static_cast<int64_t>(K) * es + moe::kTileKBytes - 1) / moe::kTileKBytes);
+  g.f16 = dtype == MOE_DT_FP16;
+  g.x_scale = x_scale;
+  g.w_scale = w_scale;
+  g.w_scale_step = w_scale_rows == 1 ? 0 : 1;
+  g.bias = bias;
+  g.bias_dt = bias_dtype;
+  g.act = act;
+  g.residual = residual;
+  g.ldr = static_cast<size_t>(ldr);
+  g.out = out;
+  g.ldo = static_cast<size_t>(ldo);
+  g.out_dt = out_dtype;
+  return fp8 ? launch_linear<true>(c, as_stream(stream)) : launch_linear<false>(c, as_stream(stream));
+}
+
+moe_status_t moe_route(const void* logits, int logits_dtype, int64_t ld, const float* bias,
+                       const uint8_t* expert_mask, const int32_t* num_valid, int T, int E, int top_k, int score,
+                       int n_group, int topk_group, int group_score, int renormalize, float routed_scaling_factor,
+                       int32_t* topk_ids, float* topk_weights, moe_stream_t stream) {
+  if (!is_float_dt(logits_dtype)) return MOE_ERR_UNSUPPORTED_DTYPE;
+  if (T < 0 || E < 1 || E > MOE_MAX_EXPERTS || top_k < 1 || top_k > E || top_k > MOE_MAX_TOPK)
+    return MOE_ERR_INVALID_ARG;
+  if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (group_score != MOE_GROUP_TOP2 && group_score != MOE_GROUP_MAX) return MOE_ERR_INVALID_ARG;
+  if (n_group < 1 || n_group > 32 || E % n_group != 0 || topk_group < 1 || topk_group > n_group ||
+      top_k > topk_group * (E / n_group))
+    return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_ids || !topk_weights || ld < E) return MOE_ERR_INVALID_ARG;
+  if (!aligned_to(logits, float_size(logits_dtype)) || !aligned_to(bias, 4) || !aligned_to(num_valid, 4) ||
+      !aligned_to(topk_ids, 4) || !aligned_to(topk_weights, 4))
+    return MOE_ERR_ALIGNMENT;
+  moe::RouteArgs a{logits, static_cast<size_t>(ld), logits_dtype, bias, expert_mask, num_valid, T, E, top_k,
+                   n_group, topk_group, group_score == MOE_GROUP_MAX, renormalize, routed_scaling_factor, topk_ids,
+                   topk_weights};
+  const bool softmax = score == MOE_SCORE_SOFTMAX;
+  cudaStream_t s = as_stream(stream);
+  if (E <= 32) return launch_route<1>(a, softmax, s);
+  if (E <= 64) return launch_route<2>(a, softmax, s);
+  if (E <= 128) return launch_route<4>(a, softmax, s);
+  if (E <= 256) return launch_route<8>(a, softmax, s);
+  return launch_route<16>(a, softmax, s);
+}
+
+moe_status_t moe_rmsnorm_quantize(int dtype, int quant, const void* x, const void* residual, const void* gamma,
+                                  int gamma_dtype, float eps, int T, int H, void* residual_out, void* y, void* codes,
+                                  void* scale, moe_stream_t stream) {
+  if (!is_16bit(dtype) || (gamma_dtype != dtype && gamma_dtype != MOE_DT_F32)) return MOE_ERR_UNSUPPORTED_DTYPE;
+  const bool fp8 = quant == MOE_DT_FP8_E4M3, mx = quant == MOE_DT_MXFP8_E4M3;
+  if (quant != MOE_DT_NONE && !fp8 && !mx) return MOE_ERR_UNSUPPORTED_DTYPE;
+  if (T < 0 || H < 1 || !(eps > 0.f)) return MOE_ERR_INVALID_ARG;
+  if (H % (mx ? 32 : 8) != 0 || H > 16384) return MOE_ERR_SHAPE;
+  if (T == 0) return MOE_OK;
+  if (!x || !gamma || (!residual_out && !y && quant == MOE_DT_NONE)) return MOE_ERR_INVALID_ARG;
+  if ((quant != MOE_DT_NONE) != (codes != nullptr) || (codes != nullptr) != (scale != nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(gamma) || !aligned16(residual_out) || !aligned16(y) ||
+      !aligned_to(codes, 8) || (fp8 && !aligned_to(scale, 4)))
+    return MOE_ERR_ALIGNMENT;
+  moe::NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.gamma = gamma;
+  a.gamma_f32 = gamma_dtype == MOE_DT_F32;
+  a.eps = eps;
+  a.T = T;
+  a.H = H;
+  a.residual_out = residual_out;
+  a.y = y;
+  a.codes = static_cast<uint8_t*>(codes);
+  if (fp8) a.scale = static_cast<float*>(scale);
+  else a.sbytes = static_cast<uint8_t*>(scale);
+  const int q = fp8 ? moe::kNormFp8 : mx ? moe::kNormMx : moe::kNormPlain;
+  cudaStream_t s = as_stream(stream);
+  return dtype == MOE_DT_BF16 ? launch_rmsnorm_quant<__nv_bfloat16>(a, q, s) : launch_rmsnorm_quant<__half>(a, q, s);
 }
 
 }  // extern "C"

@@ -1,0 +1,179 @@
+// norm.cuh - residual add, RMS norm and quantisation in one pass.
+//
+//   z = x + residual                    (fp32)       residual_out = round(z)
+//   y = z * rsqrt(mean(z^2) + eps) * gamma           (fp32)
+//   y rounded once to x's type, and / or quantised from the unrounded y to the
+//   layer's operand formats: e4m3 codes with one fp32 scale per row, or MXFP8
+//   (e4m3 codes, one ue8m0 byte per 32 columns).
+//
+// The norm reads the unrounded z, so that y carries one rounding, not two.
+//
+// What bounds it: bytes. Every operand is read once and every output written
+// once; a row stays in registers between the sum and the stores. TPR threads
+// share a row, V 16-byte chunks (8 values) each; narrow rows are packed several
+// to a block of 256 threads so that a block always has 256 threads' loads in
+// flight.
+#pragma once
+#include "quant.cuh"
+#include "router.cuh"
+
+namespace moe {
+
+enum NormQuant : int { kNormPlain = 0, kNormFp8 = 1, kNormMx = 2 };
+
+struct NormArgs {
+  const void* x;         // [T, H] bf16 or fp16
+  const void* residual;  // [T, H] or nullptr
+  const void* gamma;     // [H]: x's type, or fp32 with gamma_f32
+  int gamma_f32;
+  float eps;
+  int T, H;
+  void* residual_out;  // [T, H] or nullptr
+  void* y;             // [T, H] or nullptr
+  uint8_t* codes;      // [T, H] (kNormFp8, kNormMx)
+  float* scale;        // [T] (kNormFp8)
+  uint8_t* sbytes;     // [T, H / 32] (kNormMx)
+};
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __nv_bfloat16) {
+  return static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(lo))) |
+         (static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(hi))) << 16);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __half) {
+  return static_cast<uint32_t>(__half_as_ushort(__float2half_rn(lo))) |
+         (static_cast<uint32_t>(__half_as_ushort(__float2half_rn(hi))) << 16);
+}
+
+template <typename TX>
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  unpack2(v.x, TX(), f[0], f[1]);
+  unpack2(v.y, TX(), f[2], f[3]);
+  unpack2(v.z, TX(), f[4], f[5]);
+  unpack2(v.w, TX(), f[6], f[7]);
+}
+template <typename TX>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack2(f[0], f[1], TX()), pack2(f[2], f[3], TX()), pack2(f[4], f[5], TX()),
+                    pack2(f[6], f[7], TX()));
+}
+
+// Sum or maximum over the TPR threads of a row. `sm`: one float per warp of
+// the block; a second call in one kernel takes another array.
+template <int TPR, bool MAX>
+__device__ __forceinline__ float row_reduce(float v, float* sm) {
+#pragma unroll
+  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
+    const float u = __shfl_xor_sync(0xffffffffu, v, o);
+    v = MAX ? fmaxf(v, u) : v + u;
+  }
+  if constexpr (TPR > 32) {
+    constexpr int W = TPR / 32;
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) sm[warp] = v;
+    __syncthreads();
+    const int w0 = warp / W * W;
+    v = sm[w0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v = MAX ? fmaxf(v, sm[w0 + w]) : v + sm[w0 + w];
+  }
+  return v;
+}
+
+template <typename TX, int Q, int TPR, int V>
+__global__ void __launch_bounds__(TPR > 256 ? TPR : 256) k_rmsnorm(const NormArgs a) {
+  constexpr int kThreads = TPR > 256 ? TPR : 256;
+  __shared__ float sum_sm[kThreads / 32], max_sm[kThreads / 32];
+  const int sub = threadIdx.x % TPR;
+  const int t = blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
+  const bool row = t < a.T;  // the last block's spare rows only take part in its barriers
+  const int nc = row ? a.H / 8 : 0;
+  const size_t base = static_cast<size_t>(row ? t : 0) * a.H;
+  const uint4* x = reinterpret_cast<const uint4*>(static_cast<const TX*>(a.x) + base);
+  const uint4* r = a.residual ? reinterpret_cast<const uint4*>(static_cast<const TX*>(a.residual) + base) : nullptr;
+
+  uint4 xv[V], rv[V], gv[V];
+#pragma unroll
+  for (int u = 0; u < V; ++u) {
+    const int c = sub + u * TPR;
+    xv[u] = c < nc ? x[c] : make_uint4(0, 0, 0, 0);
+    rv[u] = r && c < nc ? r[c] : make_uint4(0, 0, 0, 0);
+    gv[u] = !a.gamma_f32 && c < nc ? __ldg(static_cast<const uint4*>(a.gamma) + c) : make_uint4(0, 0, 0, 0);
+  }
+  float z[V][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int u = 0; u < V; ++u) {
+    const int c = sub + u * TPR;
+    unpack8<TX>(xv[u], z[u]);
+    if (r) {
+      float f[8];
+      unpack8<TX>(rv[u], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[u][i] += f[i];
+    }
+    if (a.residual_out && c < nc)
+      reinterpret_cast<uint4*>(static_cast<TX*>(a.residual_out) + base)[c] = pack8<TX>(z[u]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(z[u][i], z[u][i], ss);
+  }
+  ss = row_reduce<TPR, false>(ss, sum_sm);
+  const float rstd = rsqrtf(ss / static_cast<float>(a.H) + a.eps);
+
+  float amax = 0.f;
+#pragma unroll
+  for (int u = 0; u < V; ++u) {
+    const int c = sub + u * TPR;
+    float g[8];
+    if (a.gamma_f32) {
+      const float4* gp = static_cast<const float4*>(a.gamma) + 2 * c;
+      const float4 lo = c < nc ? __ldg(gp) : make_float4(0, 0, 0, 0);
+      const float4 hi = c < nc ? __ldg(gp + 1) : make_float4(0, 0, 0, 0);
+      g[0] = lo.x, g[1] = lo.y, g[2] = lo.z, g[3] = lo.w;
+      g[4] = hi.x, g[5] = hi.y, g[6] = hi.z, g[7] = hi.w;
+    } else {
+      unpack8<TX>(gv[u], g);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[u][i] = z[u][i] * rstd * g[i];
+    if (a.y && c < nc) reinterpret_cast<uint4*>(static_cast<TX*>(a.y) + base)[c] = pack8<TX>(z[u]);
+    if (Q != kNormPlain) {
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(z[u][i]));
+      if (Q == kNormFp8) {
+        amax = fmaxf(amax, m);
+      } else {
+        // 32 columns = the chunks of four consecutive lanes (H % 32 == 0: in or out together)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        if (c < nc) {
+          const int X = mx_exponent_bits(m);
+          const float f = pow2_neg(X);  // exact: a power of two in the normal range
+          uint32_t q[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) q[i] = cvt_e4m3x2(z[u][2 * i] * f, z[u][2 * i + 1] * f);
+          reinterpret_cast<uint2*>(a.codes + base)[c] = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+          if ((threadIdx.x & 3) == 0)
+            a.sbytes[static_cast<size_t>(t) * (a.H / 32) + c / 4] = static_cast<uint8_t>(X + 127);
+        }
+      }
+    }
+  }
+  if (Q == kNormFp8) {
+    amax = row_reduce<TPR, true>(amax, max_sm);
+    const float s = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+    if (row && sub == 0) a.scale[t] = s;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      const int c = sub + u * TPR;
+      if (c < nc) {
+        uint32_t q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = cvt_e4m3x2(__fdiv_rn(z[u][2 * i], s), __fdiv_rn(z[u][2 * i + 1], s));
+        reinterpret_cast<uint2*>(a.codes + base)[c] = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+      }
+    }
+  }
+}
+
+}  // namespace moe

@@ -21,6 +21,10 @@ enum DeviceErr : int {
   kErrBlockExpert = 4,
 };
 
+// Routing id of a padding row of a batch: the sort drops its slots without an
+// error, so that no expert works on them.
+constexpr int32_t kNoExpert = INT32_MIN;
+
 // A wait longer than this is treated as a hang: the kernel records
 // kErrWaitTimeout and unwinds instead of spinning forever.
 constexpr uint64_t kWaitTimeoutNs = 4000000000ull;

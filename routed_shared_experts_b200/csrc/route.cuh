@@ -1,0 +1,235 @@
+// route.cuh - expert routing in its general form, one warp per token.
+//
+//   s_e = softmax(l)_e over the live experts, or sigmoid(l_e)
+//   c_e = fp32(s_e) + bias_e                           (what the choice goes by)
+//   group score = c of the group's best live expert, or the sum of its two best
+//   keep the topk_group best groups, pick k experts of them by c
+//   w_j = s_j / sum of the picked s (renormalize) or s_j, times the scaling factor
+//
+// Scores are evaluated in double and rounded to fp32 once: the choice between
+// two neighbours then depends on one rounding of a value that any machine
+// reproduces to far below it, and never on the order of a sum. The weights are
+// taken from the unrounded scores and rounded once at the end.
+//
+// An expert is dead for a token when its mask is 0, its logit is NaN or -inf,
+// or its c is NaN or -inf (a bias of -inf switches an expert off). Dead
+// experts are picked last, lowest index first, with weight 0: a row always
+// gets k distinct experts, so that the slots of the layer's sort and the
+// arrival counts of its stage 2 stay complete whatever the mask leaves.
+//
+// What bounds it: latency, not bytes (a 256-expert fp32 row is 1 KB). The
+// chain is load -> double exp -> (max, sum) -> group choice -> k rounds of
+// arg-max, so the rounds are kept short: c is mapped to an unsigned key with
+// the same order and one round is a redux.max of the key and a redux.min of
+// the index among the lanes that hold it, with each lane's best key kept
+// between rounds.
+#pragma once
+#include "router.cuh"
+
+namespace moe {
+
+struct RouteArgs {
+  const void* logits;  // [T, E], rows ld apart
+  size_t ld;
+  int dtype;                 // MOE_DT_F32, MOE_DT_BF16 or MOE_DT_FP16
+  const float* bias;         // [E] or nullptr
+  const uint8_t* mask;       // [E], 0 = dead, or nullptr
+  const int32_t* num_valid;  // rows from *num_valid on are padding, or nullptr
+  int T, E, k, n_group, topk_group, group_max, renormalize;
+  float rsf;
+  int32_t* ids;  // [T, k]
+  float* wts;    // [T, k]
+};
+
+constexpr int kRouteWarps = 4;
+
+// Order-preserving key of a float that is not NaN. -inf maps to kDeadKey,
+// every larger value above it; 0 is left for experts that cannot be picked.
+constexpr uint32_t kDeadKey = 0x007fffffu;
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);  // -0 and +0 rank as equals
+  return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+
+__device__ __forceinline__ float route_logit(const RouteArgs& a, size_t row, int e) {
+  if (a.dtype == 4) return __ldg(static_cast<const float*>(a.logits) + row + e);
+  const unsigned short b = __ldg(static_cast<const unsigned short*>(a.logits) + row + e);
+  return a.dtype == 0 ? __bfloat162float(__ushort_as_bfloat16(b)) : __half2float(__ushort_as_half(b));
+}
+
+// exp(l - mx) with the limit of equal infinities taken as 1.
+__device__ __forceinline__ double route_exp(float l, float mx) {
+  return l == mx ? 1.0 : exp(static_cast<double>(l) - static_cast<double>(mx));
+}
+
+// Lanes that share a group in the group choice: 32 / (n_group rounded up to a
+// power of two); the group's values lie `stride` words apart in shared memory,
+// with stride % 32 == lanes so that the 32 lanes read 32 banks.
+struct RouteGroups {
+  int size, lanes, stride;
+  __host__ __device__ RouteGroups(int E, int n_group) {
+    int p = 1;
+    while (p < n_group) p *= 2;
+    size = E / n_group;
+    lanes = 32 / p;
+    stride = size + ((lanes - size) % 32 + 32) % 32;
+  }
+  __host__ __device__ size_t smem_words(int n_group) const { return static_cast<size_t>(n_group) * stride; }
+};
+
+template <int VPL, bool SOFTMAX>
+__global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
+  extern __shared__ float route_sm[];  // per warp: c by group (n_group > 1)
+  const int wib = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int t = blockIdx.x * kRouteWarps + wib;
+  if (t >= a.T) return;
+  const size_t out = static_cast<size_t>(t) * a.k + lane;
+  if (a.num_valid && t >= __ldg(a.num_valid)) {
+    if (lane < a.k) {
+      a.ids[out] = kNoExpert;
+      a.wts[out] = 0.f;
+    }
+    return;
+  }
+  const float NEG_INF = __int_as_float(0xff800000);
+  const size_t row = static_cast<size_t>(t) * a.ld;
+
+  // scores of this lane's experts e = lane + 32 i
+  float l[VPL];
+  float mx = NEG_INF;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane + 32 * i;
+    l[i] = NEG_INF;
+    if (e < a.E && !(a.mask && __ldg(a.mask + e) == 0)) {
+      const float v = route_logit(a, row, e);
+      if (v == v) l[i] = v;
+    }
+    mx = fmaxf(mx, l[i]);
+  }
+  double inv_z = 1.0;
+  uint32_t key[VPL];
+  if (SOFTMAX) {
+    mx = warp_max_f(mx);
+    double p[VPL];
+    double z = 0.0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      p[i] = l[i] == NEG_INF ? 0.0 : route_exp(l[i], mx);
+      z += p[i];
+    }
+    z = warp_sum_d(z);
+    inv_z = z > 0.0 ? 1.0 / z : 0.0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = __float_as_uint(static_cast<float>(p[i] * inv_z));
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      key[i] = __float_as_uint(static_cast<float>(1.0 / (1.0 + exp(-static_cast<double>(l[i])))));
+  }
+  // c, then its key; positions past E take no part (key 0)
+  const RouteGroups G(a.E, a.n_group);
+  float* c_sm = route_sm + static_cast<size_t>(wib) * G.smem_words(a.n_group);
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane + 32 * i;
+    float c = __uint_as_float(key[i]);
+    key[i] = 0;
+    if (e < a.E) {
+      if (a.bias) c = __fadd_rn(c, __ldg(a.bias + e));
+      if (l[i] == NEG_INF || c != c) c = NEG_INF;
+      key[i] = order_key(c);
+      if (a.n_group > 1) {
+        const int g = e / G.size;
+        c_sm[g * G.stride + (e - g * G.size)] = c;
+      }
+    }
+  }
+
+  if (a.n_group > 1) {
+    __syncwarp();
+    // two best values of this lane's share of group g, merged over its lanes
+    const int g = lane / G.lanes;
+    const int sub = lane - g * G.lanes;
+    float m1 = NEG_INF, m2 = NEG_INF;
+    if (g < a.n_group) {
+      for (int j = sub; j < G.size; j += G.lanes) {
+        const float v = c_sm[g * G.stride + j];
+        m2 = fmaxf(m2, fminf(m1, v));
+        m1 = fmaxf(m1, v);
+      }
+    }
+    for (int o = 1; o < G.lanes; o *= 2) {
+      const float o1 = __shfl_xor_sync(0xffffffffu, m1, o);
+      const float o2 = __shfl_xor_sync(0xffffffffu, m2, o);
+      m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
+      m1 = fmaxf(m1, o1);
+    }
+    // a group with one live expert scores that expert alone
+    const float score = (a.group_max || m2 == NEG_INF) ? m1 : __fadd_rn(m1, m2);
+    uint32_t gkey = (sub == 0 && g < a.n_group) ? order_key(score) : 0;
+    uint32_t kept = 0;  // by group
+    for (int r = 0; r < a.topk_group; ++r) {
+      const uint32_t best = __reduce_max_sync(0xffffffffu, gkey);
+      const int win = __ffs(__ballot_sync(0xffffffffu, gkey == best)) - 1;  // lowest lane = lowest group
+      if (lane == win) gkey = 0;
+      kept |= 1u << (win / G.lanes);
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = lane + 32 * i;
+      if (e < a.E && !((kept >> (e / G.size)) & 1u)) key[i] = 0;
+    }
+  }
+
+  // k rounds; lane j keeps the j-th pick. best / bi: this lane's best key and
+  // the lowest slot that holds it.
+  uint32_t best = 0;
+  int bi = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    if (key[i] > best) {
+      best = key[i];
+      bi = i;
+    }
+  int sel = 0;
+  bool live = false;
+  for (int j = 0; j < a.k; ++j) {
+    const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+    const unsigned e = __reduce_min_sync(0xffffffffu, best == m ? static_cast<unsigned>(lane + 32 * bi) : 0xffffffffu);
+    if (lane == j) {
+      sel = static_cast<int>(e);
+      live = m > kDeadKey;
+    }
+    if (lane == static_cast<int>(e & 31u)) {  // this lane's next best
+      const int gone = static_cast<int>(e >> 5);
+      best = 0;
+      bi = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        if (i == gone) key[i] = 0;
+        if (key[i] > best) {
+          best = key[i];
+          bi = i;
+        }
+      }
+    }
+  }
+
+  double p = 0.0;
+  if (lane < a.k && live) {
+    const float v = route_logit(a, row, sel);
+    p = SOFTMAX ? route_exp(v, mx) * inv_z : 1.0 / (1.0 + exp(-static_cast<double>(v)));
+  }
+  if (a.renormalize) {
+    const double sum = warp_sum_d(p);
+    p = sum > 0.0 ? p / sum : 0.0;
+  }
+  if (lane < a.k) {
+    a.ids[out] = sel;
+    a.wts[out] = static_cast<float>(p * static_cast<double>(a.rsf));
+  }
+}
+
+}  // namespace moe

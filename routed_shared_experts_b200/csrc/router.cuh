@@ -458,6 +458,11 @@ __global__ void k_append_shared_slots(const int32_t* __restrict__ ids, const flo
     ids2[i] = ids[static_cast<size_t>(t) * k + j];
     w2[i] = w[static_cast<size_t>(t) * k + j];
   } else {
+    if (ids[static_cast<size_t>(t) * k] == kNoExpert) {  // a padding row takes no shared slot either
+      ids2[i] = kNoExpert;
+      w2[i] = 0.0f;
+      return;
+    }
     ids2[i] = E + (j - k);
     float g = 1.0f;
     if (gate) g = gate_half ? __half2float(static_cast<const __half*>(gate)[t])

@@ -62,7 +62,7 @@ __device__ __forceinline__ void sort_count(const SortArgs& a, int f0, int f1, in
     for (int u = 0; u < B; ++u) {
       const int f = b0 + 32 * u + lane;
       int e = ev[u];
-      if (e >= a.E || (f < f1 && e < 0)) {
+      if (e >= a.E || (f < f1 && e < 0 && e != kNoExpert)) {
         set_device_error(kErrExpertRange);
         e = -1;
       }

@@ -1,0 +1,250 @@
+"""moe_linear against the formula in 64 bits.
+
+Two kinds of cases. With small whole numbers every partial sum is exact in
+fp32 whatever its order, so the result is the formula's value rounded once: the
+comparison is for equality, over the shapes and strides where tiles, K splits
+and tails can go wrong. With random values the tolerance is
+
+    u |y|                 the store's rounding (u = eps / 2 of the output type)
+  + 1.2 * dpre            the accumulator's error through the activation
+                          (every activation's slope is below 1.2)
+  + 2^-19 |act|           the fast exponential and division
+  + 2^-23 (|act| + |res|) the residual add
+
+with dpre = 2^-23 (K / 8 + 8) sum|x w| scales + 2^-23 |bias|: an MMA adds 16
+(or 32) products to the accumulator, each of those K / 16 additions and the few
+of the K split off by at most two units of the last place of a partial sum that
+sum|x w| bounds, plus the scale products.
+"""
+import math
+
+import pytest
+import torch
+
+from routed_shared_experts_b200 import capi
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "f32": torch.float32, "fp8": torch.float8_e4m3fn}
+GUARD = 77.0
+
+
+def _wide(v, pad, dtype):
+    """v as a view into a wider buffer filled with GUARD, and the buffer."""
+    R, C = v.shape
+    if pad == 0:
+        b = v.to(dtype).cuda().contiguous()
+        return b, None
+    off = 16
+    b = torch.full((R, C + off + pad), GUARD, dtype=torch.float32).to(dtype).cuda()
+    b[:, off:off + C] = v.to(dtype).cuda()
+    return b[:, off:off + C], b
+
+
+def _act64(v, act):
+    if act == "relu":
+        return torch.where(v < 0, torch.zeros_like(v), v)
+    if act == "silu":
+        return v / (1 + torch.exp(-v))
+    if act == "gelu":
+        return 0.5 * v * torch.special.erfc(-v / math.sqrt(2))
+    if act == "gelu_tanh":
+        return 0.5 * v * (1 + torch.tanh(math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3)))
+    if act == "sigmoid":
+        return 1 / (1 + torch.exp(-v))
+    return v
+
+
+def _reference(x, w, xs, ws, b, act, r):
+    """(value, dpre, act) in float64 on the host."""
+    x, w = x.double().cpu(), w.double().cpu()
+    pre = x @ w.t()
+    mag = x.abs() @ w.abs().t()
+    if xs is not None:
+        s = xs.double().cpu()[:, None] * ws.double().cpu()[None, :]
+        pre, mag = pre * s, mag * s
+    d = 2.0 ** -23 * (x.shape[1] / 8 + 8) * mag
+    if b is not None:
+        pre = pre + b.double().cpu()
+        d = d + 2.0 ** -23 * b.double().cpu().abs()
+    a = _act64(pre, act)
+    return (a if r is None else a + r.double().cpu()), d, a
+
+
+def _run(T, N, K, dt, odt, bias=None, act="none", residual=False, pad=0, ints=False, seed=0, one_scale=False,
+         in_place=False, stream=None):
+    g = torch.Generator().manual_seed(1000 * T + 10 * N + K + seed)
+    if ints:
+        x = torch.randint(-3, 4, (T, K), generator=g).float()
+        w = torch.randint(-3, 4, (N, K), generator=g).float()
+    else:
+        x, w = torch.randn((T, K), generator=g), torch.randn((N, K), generator=g) * 0.05
+    xs = ws = None
+    if dt == "fp8":
+        xs = (2.0 ** torch.randint(-2, 3, (T,), generator=g)).float() if ints else torch.rand(T, generator=g) + 0.5
+        n_ws = 1 if one_scale else N
+        ws = (2.0 ** torch.randint(-2, 3, (n_ws,), generator=g)).float() if ints else torch.rand(n_ws, generator=g) + 0.5
+    xv, _ = _wide(x, pad, DT[dt])
+    wv, _ = _wide(w, pad, DT[dt])
+    b = r = rv = None
+    if bias:
+        b = (torch.randint(-8, 9, (N,), generator=g).float() if ints else torch.randn(N, generator=g)).to(DT[bias]).cuda()
+    if residual:
+        r = torch.randint(-9, 10, (T, N), generator=g).float() if ints else torch.randn((T, N), generator=g)
+        rv, _ = _wide(r, pad, DT[odt])
+    ov, ob = _wide(torch.full((T, N), -55.0), pad, DT[odt])
+    if in_place:
+        ov.copy_(rv)
+        rv_call = ov
+        r_ref = rv.clone()
+    else:
+        rv_call, r_ref = rv, rv
+    xs_d = None if xs is None else xs.cuda()
+    ws_d = None if ws is None else ws.cuda()
+    capi.moe_linear(capi.DTYPES[dt], xv, xs_d, wv, ws_d, b, capi.ACTS[act], rv_call, ov, stream)
+    torch.cuda.synchronize()
+    assert capi.device_error() == 0
+    ref, d, a = _reference(xv, wv, xs, None if ws is None else ws.expand(N), b, act, r_ref)
+    if ob is not None:  # nothing between the rows is written
+        assert torch.all(ob[:, :16].float() == GUARD) and torch.all(ob[:, 16 + N:].float() == GUARD)
+    return ov, ref, d, a, r_ref
+
+
+def _check(T, N, K, dt, odt, **kw):
+    out, ref, d, a, r = _run(T, N, K, dt, odt, **kw)
+    if kw.get("ints"):
+        want = ref.to(DT[odt]) if odt != "f32" else ref.float()
+        assert torch.equal(out.cpu(), want), (T, N, K, (out.cpu().double() - ref).abs().max())
+        return
+    u = torch.finfo(DT[odt]).eps / 2
+    tol = u * ref.abs() + 1.2 * d + 2.0 ** -19 * a.abs() + 2.0 ** -23 * (a.abs() + (0 if r is None else r.double().cpu().abs()))
+    tol = tol + torch.finfo(DT[odt]).smallest_normal * u  # half a subnormal step
+    err = (out.double().cpu() - ref).abs()
+    assert torch.all(err <= tol), (T, N, K, (err / tol).max())
+
+
+# every token tile width with one row, a row short, full and one over; outputs below, at and past a
+# 128-row tile and odd; K of less than an atom, one atom, ragged atoms and long enough for each K split
+SHAPES = [(1, 1, 8), (1, 128, 64), (1, 2048, 2048), (2, 129, 72), (15, 127, 136), (16, 128, 512), (17, 256, 1024),
+          (31, 33, 520), (32, 7168, 256), (33, 640, 2048), (63, 65, 4096), (64, 1000, 264), (65, 384, 1032),
+          (127, 255, 128), (128, 128, 7168), (129, 257, 192), (255, 1409, 320), (256, 512, 2816), (257, 130, 640),
+          (300, 2815, 408), (511, 768, 1408), (513, 77, 2056), (1000, 1000, 1000), (1024, 512, 16), (2049, 384, 200),
+          (4096, 256, 512), (1, 20000, 64), (4097, 8, 64)]
+
+
+@pytest.mark.parametrize("T,N,K", SHAPES)
+def test_linear_exact_bf16(cuda_lib, T, N, K):
+    _check(T, N, K, "bf16", "f32", ints=True)
+
+
+@pytest.mark.parametrize("T,N,K", SHAPES)
+@pytest.mark.parametrize("dt,odt", [("bf16", "bf16"), ("fp16", "fp16"), ("fp16", "f32")])
+def test_linear_exact_epilogue(cuda_lib, T, N, K, dt, odt):
+    """Bias, residual, ReLU and strides; whole numbers, so one rounding."""
+    _check(T, N, K, dt, odt, ints=True, bias="f32", act="relu", residual=True, pad=24 if N % 2 else 0)
+
+
+@pytest.mark.parametrize("T,N,K", [(t, n, -(-k // 16) * 16) for t, n, k in SHAPES])
+@pytest.mark.parametrize("odt", ["f32", "bf16", "fp16"])
+def test_linear_exact_fp8(cuda_lib, T, N, K, odt):
+    _check(T, N, K, "fp8", odt, ints=True, bias="bf16", residual=T % 2 == 1, pad=16 if T % 3 == 0 else 0,
+           one_scale=N % 2 == 0)
+
+
+@pytest.mark.parametrize("act", sorted(capi.ACTS))
+@pytest.mark.parametrize("T,N,K,dt,odt", [(3, 200, 512, "bf16", "f32"), (70, 333, 2048, "fp16", "fp16"),
+                                          (515, 1100, 1024, "bf16", "bf16"), (40, 96, 4096, "fp8", "f32"),
+                                          (600, 514, 640, "fp8", "bf16")])
+def test_linear_random(cuda_lib, act, T, N, K, dt, odt):
+    _check(T, N, K, dt, odt, bias="f32", act=act, residual=True)
+
+
+@pytest.mark.parametrize("T,N,K,dt,odt", [(1, 2048, 7168, "bf16", "f32"), (4096, 256, 7168, "bf16", "f32"),
+                                          (777, 2815, 4096, "fp16", "fp16"), (1024, 5632, 4096, "fp8", "bf16")])
+def test_linear_long_k(cuda_lib, T, N, K, dt, odt):
+    _check(T, N, K, dt, odt, bias="bf16", pad=8 if dt != "fp8" else 16)
+
+
+@pytest.mark.parametrize("T", [1, 20, 100, 300, 2000])
+def test_linear_residual_in_place(cuda_lib, T):
+    for odt in ("bf16", "f32"):
+        _check(T, 640, 512, "bf16", odt, ints=True, residual=True, in_place=True, pad=8)
+        _check(T, 333, 512, "bf16", odt, ints=True, residual=True, in_place=True)
+
+
+@pytest.mark.parametrize("T,N,K", [(5, 300, 256), (600, 520, 256)])
+def test_linear_infinities_and_nan(cuda_lib, T, N, K):
+    """Infinities and NaN of an operand reach exactly the outputs they belong
+    to, through every activation as the formula has it."""
+    for act in sorted(capi.ACTS):
+        g = torch.Generator().manual_seed(3)
+        x, w = torch.randn((T, K), generator=g).to(torch.bfloat16), torch.randn((N, K), generator=g).to(torch.bfloat16)
+        x[1, 3], x[2, 200], w[7, 9] = float("inf"), float("nan"), float("-inf")
+        out = torch.zeros((T, N), dtype=torch.float32, device="cuda")
+        capi.moe_linear(capi.MOE_DT_BF16, x.cuda(), None, w.cuda(), None, None, capi.ACTS[act], None, out)
+        torch.cuda.synchronize()
+        v = x.float() @ w.float().t()
+        ref = _act64(v, act)  # fp32 has the same infinities and NaN
+        got = out.cpu()
+        assert torch.equal(torch.isnan(got), torch.isnan(ref)), act
+        assert torch.equal(got[torch.isinf(ref)], ref[torch.isinf(ref)]), act
+
+
+def test_linear_no_rows(cuda_lib):
+    x = torch.zeros((0, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((8, 64), dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros((0, 8), dtype=torch.bfloat16, device="cuda")
+    capi.moe_linear(capi.MOE_DT_BF16, x, None, w, None, None, 0, None, out)
+    torch.cuda.synchronize()
+
+
+def test_linear_wrapper_refusals(cuda_lib):
+    x = torch.zeros((4, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((8, 64), dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros((4, 8), dtype=torch.bfloat16, device="cuda")
+    bf = capi.MOE_DT_BF16
+    with pytest.raises(TypeError):
+        capi.moe_linear(capi.MOE_DT_FP16, x, None, w, None, None, 0, None, out)
+    with pytest.raises(ValueError):
+        capi.moe_linear(bf, x, None, w[:, :32], None, None, 0, None, out)
+    with pytest.raises(ValueError):
+        capi.moe_linear(bf, x, None, w, None, None, 0, None, out.t())
+    with pytest.raises(TypeError):
+        capi.moe_linear(bf, x, None, w, None, None, 0, out.float(), out)
+    with pytest.raises(ValueError):  # an expanded operand's rows overlap
+        capi.moe_linear(bf, x[:1].expand(4, 64), None, w, None, None, 0, None, out)
+    with pytest.raises(capi.MoEError):  # rows of 66 values are not 16-byte aligned
+        y = torch.zeros((4, 66), dtype=torch.bfloat16, device="cuda")[:, :64]
+        capi.moe_linear(bf, y, None, w, None, None, 0, None, out)
+    with pytest.raises(capi.MoEError):
+        capi.moe_linear(bf, x, None, w, None, None, 17, None, out)
+
+
+@pytest.mark.parametrize("T,N,K", [(8, 512, 2048), (700, 1100, 512)])
+def test_linear_repeatable_and_concurrent(cuda_lib, T, N, K):
+    """The same bits every time, two calls at once on two streams included, and
+    from a captured graph replayed on new inputs."""
+    g = torch.Generator().manual_seed(9)
+    xs = [torch.randn((T, K), generator=g).to(torch.bfloat16).cuda() for _ in range(2)]
+    w = (torch.randn((N, K), generator=g) * 0.05).to(torch.bfloat16).cuda()
+    call = lambda x, o, s=None: capi.moe_linear(capi.MOE_DT_BF16, x, None, w, None, None, 2, None, o, s)  # noqa: E731
+    want = [torch.empty((T, N), dtype=torch.float32, device="cuda") for _ in range(2)]
+    for x, o in zip(xs, want):
+        call(x, o)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [torch.empty_like(want[0]) for _ in range(2)]
+    for _ in range(20):
+        for x, o, s in zip(xs, got, streams):
+            call(x, o, s)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    x, o = xs[0].clone(), torch.empty_like(want[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(x, o)
+    for i in (1, 0, 1):
+        x.copy_(xs[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[i])

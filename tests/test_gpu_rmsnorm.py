@@ -1,0 +1,189 @@
+"""moe_rmsnorm_quantize against the formula in 64 bits.
+
+Tolerances: the sum of squares is off by at most 50 units of 2^-24 (up to 32
+fused additions per thread, ten in the reductions, the division), half of which
+reach 1/rms; the square root, two products and z's own rounding add a few, so
+the unrounded y is within 2^-18 of the formula, relative to |y| plus the
+cancellation of z: 2^-24 (|x| + |residual|) through the same factor. The 16-bit
+store adds half a step of its type, a code half a step of e4m3 (2^-4, or 2^-10
+in its subnormal range), measured in units of the scale; values past 448 units
+saturate."""
+import math
+
+import pytest
+import torch
+
+from routed_shared_experts_b200 import capi
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+QUANT = {"none": None, "fp8": capi.MOE_DT_FP8_E4M3, "mxfp8": capi.MOE_DT_MXFP8_E4M3}
+
+
+def _inputs(T, H, dt, seed=0):
+    g = torch.Generator().manual_seed(100 * T + H + seed)
+    x, r = torch.randn((T, H), generator=g), 3 * torch.randn((T, H), generator=g)
+    gamma = 1 + 0.3 * torch.randn(H, generator=g)
+    if T > 3:
+        x[1], r[1] = 0, 0             # a row of zeros
+        x[2, 7 % H] = 300.0           # an outlier
+        x[3, :32], r[3, :32] = 0, 0   # a block of zeros
+    return x.to(DT[dt]), r.to(DT[dt]), gamma.to(DT[dt])
+
+
+def _check(T, H, dt, quant, residual=True, y=True, gamma_f32=False, eps=1e-6):
+    x, r, gamma = _inputs(T, H, dt)
+    if gamma_f32:
+        gamma = gamma.float() * 1.001
+    dev = dict(device="cuda")
+    res = r.cuda() if residual else None
+    ro = torch.empty((T, H), dtype=DT[dt], **dev) if residual else None
+    yo = torch.empty((T, H), dtype=DT[dt], **dev) if y else None
+    codes = scale = None
+    if quant != "none":
+        codes = torch.empty((T, H), dtype=torch.uint8, **dev)
+        scale = torch.empty(T, **dev) if quant == "fp8" else torch.empty((T, H // 32), dtype=torch.uint8, **dev)
+    capi.moe_rmsnorm_quantize(QUANT[quant], x.cuda(), res, gamma.cuda(), eps, ro, yo, codes, scale)
+    torch.cuda.synchronize()
+    z = x.double() + (r.double() if residual else 0)
+    if residual:  # one rounding of the fp32 sum
+        assert torch.equal(ro.cpu(), (x.float() + r.float()).to(DT[dt]))
+    rms = torch.sqrt((z * z).mean(1, keepdim=True) + eps)
+    ref = z / rms * gamma.double()
+    slack = 2.0 ** -18 * ref.abs()
+    if residual:
+        slack = slack + 2.0 ** -24 * (x.double().abs() + r.double().abs()) / rms * gamma.double().abs()
+    if y:
+        fi = torch.finfo(DT[dt])
+        tol = slack + fi.eps / 2 * (ref.abs() + slack) + fi.smallest_normal * fi.eps / 2
+        assert torch.all((yo.cpu().double() - ref).abs() <= tol)
+    if quant == "none":
+        return
+    c = codes.cpu().view(torch.float8_e4m3fn).double()
+    if quant == "fp8":
+        s = scale.cpu().double()[:, None]
+        amax = ref.abs().amax(1, keepdim=True)
+        want = torch.where(amax > 0, amax / 448, torch.ones_like(amax))
+        # the amax's own slack, and two fp32 roundings
+        assert torch.all((s - want).abs() <= slack.amax(1, keepdim=True) / 448 + 2.0 ** -22 * want)
+        unit = s
+    else:
+        sb = scale.cpu().int()
+        b = ref.view(T, -1, 32)
+        hi = (b.abs() + slack.view(T, -1, 32)).amax(2)
+        lo = (b.abs() - slack.view(T, -1, 32)).amax(2)
+        byte = lambda a: torch.where(a > 0, (torch.floor(torch.log2(a.clamp_min(1e-300))) - 8).clamp(-127, 127), -127.0).int() + 127  # noqa: E731
+        assert torch.all((sb >= byte(lo)) & (sb <= byte(hi)))
+        unit = torch.exp2(sb.double() - 127).repeat_interleave(32, 1)
+    v = (ref / unit).clamp(-448, 448)
+    tol = slack / unit + 2.0 ** -4 * (v.abs() + slack / unit) + 2.0 ** -10 + 2.0 ** -20
+    assert torch.all((c - v).abs() <= tol)
+
+
+# one chunk, every threads-per-row and chunks-per-thread variant with ragged ends, and the widest row
+WIDTHS = [8, 32, 64, 200, 256, 264, 512, 520, 1024, 1032, 2048, 2056, 4096, 4104, 7168, 8192, 8200, 14656, 16384]
+
+
+@pytest.mark.parametrize("H", WIDTHS)
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_norm(cuda_lib, H, dt):
+    _check(5, H, dt, "none")
+    _check(1, H, dt, "none", residual=False, gamma_f32=True)
+
+
+@pytest.mark.parametrize("H", WIDTHS)
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_norm_fp8(cuda_lib, H, dt):
+    _check(9, H, dt, "fp8")
+    _check(4, H, dt, "fp8", residual=False, y=False)
+
+
+@pytest.mark.parametrize("H", [h // 32 * 32 for h in WIDTHS if h >= 32])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_norm_mxfp8(cuda_lib, H, dt):
+    _check(9, H, dt, "mxfp8")
+    _check(4, H, dt, "mxfp8", residual=False, y=False, gamma_f32=True)
+
+
+@pytest.mark.parametrize("T", [1, 2, 7, 8, 9, 1000, 4097])
+@pytest.mark.parametrize("quant", ["none", "fp8", "mxfp8"])
+def test_norm_rows(cuda_lib, T, quant):
+    _check(T, 96, "bf16", quant)
+
+
+def test_norm_in_place_and_guards(cuda_lib):
+    """residual_out = residual and y = x give the same bits, and nothing behind
+    the rows is written."""
+    T, H = 13, 520
+    x, r, gamma = _inputs(T, H, "bf16")
+    xs, rs = (torch.full((T + 2, H), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    xs[:T], rs[:T] = x.cuda(), r.cuda()
+    yo, ro = torch.empty_like(xs[:T]), torch.empty_like(xs[:T])
+    capi.moe_rmsnorm_quantize(None, xs[:T], rs[:T], gamma.cuda(), 1e-5, ro, yo, None, None)
+    capi.moe_rmsnorm_quantize(None, xs[:T], rs[:T], gamma.cuda(), 1e-5, rs[:T], xs[:T], None, None)
+    torch.cuda.synchronize()
+    assert torch.equal(xs[:T], yo) and torch.equal(rs[:T], ro)
+    assert torch.all(xs[T:] == 5) and torch.all(rs[T:] == 5)
+
+
+def test_norm_infinities_and_nan(cuda_lib):
+    """A NaN spoils its own row only; an infinity gives zeros beside it and a
+    NaN in its place, as the formula does; codes of NaN are NaN codes."""
+    T, H = 4, 256
+    x, _, gamma = _inputs(T, H, "bf16", seed=1)
+    x[0, 3], x[1, 200] = float("nan"), float("inf")
+    y = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+    c, s = torch.empty((T, H), dtype=torch.uint8, device="cuda"), torch.empty(T, device="cuda")
+    capi.moe_rmsnorm_quantize(QUANT["fp8"], x.cuda(), None, gamma.cuda(), 1e-6, None, y, c, s)
+    torch.cuda.synchronize()
+    y, c = y.cpu().float(), c.cpu().view(torch.float8_e4m3fn).float()
+    assert torch.isnan(y[0]).all() and torch.isnan(c[0]).all()
+    assert torch.isnan(y[1, 200]) and torch.isnan(c[1, 200])
+    keep = torch.arange(H) != 200
+    assert torch.all(y[1][keep] == 0) and torch.all(c[1][keep] == 0)
+    assert torch.isfinite(y[2:]).all() and torch.isfinite(c[2:]).all()
+
+
+def test_norm_matches_the_quantiser(cuda_lib):
+    """With gamma such that y is exactly representable the codes and scales are
+    those of moe_quantize_activations on the stored y."""
+    T, H = 6, 512
+    x = torch.ones((T, H), dtype=torch.bfloat16, device="cuda")
+    gamma = (torch.arange(H) % 31 + 1).to(torch.bfloat16).cuda()
+    for name, sshape, sdt in (("fp8", (T,), torch.float32), ("mxfp8", (T, H // 32), torch.uint8)):
+        y = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+        c, c2 = (torch.empty((T, H), dtype=torch.uint8, device="cuda") for _ in range(2))
+        s, s2 = (torch.empty(sshape, dtype=sdt, device="cuda") for _ in range(2))
+        capi.moe_rmsnorm_quantize(QUANT[name], x, None, gamma, 2.0 ** -40, None, y, c, s)  # rms rounds to 1
+        capi.moe_quantize_activations(QUANT[name], y, c2, s2)
+        torch.cuda.synchronize()
+        assert torch.equal(y.float(), gamma.float().expand(T, H))
+        assert torch.equal(c, c2) and torch.equal(s, s2)
+
+
+def test_norm_no_rows_graph_and_refusals(cuda_lib):
+    z = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
+    g = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    capi.moe_rmsnorm_quantize(None, z, None, g, 1e-6, None, z, None, None)
+    x, y = torch.randn((4, 64), device="cuda").bfloat16(), torch.empty((4, 64), dtype=torch.bfloat16, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        capi.moe_rmsnorm_quantize(None, x, None, g, 1e-6, None, y, None, None)
+    for _ in range(2):
+        new = torch.randn((4, 64), device="cuda").bfloat16()
+        x.copy_(new)
+        graph.replay()
+        want = torch.empty_like(y)
+        capi.moe_rmsnorm_quantize(None, new, None, g, 1e-6, None, want, None, None)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+    with pytest.raises(TypeError):
+        capi.moe_rmsnorm_quantize(None, x, x.float(), g, 1e-6, None, y, None, None)
+    with pytest.raises(ValueError):
+        capi.moe_rmsnorm_quantize(None, x, None, g[:32], 1e-6, None, y, None, None)
+    with pytest.raises(ValueError):
+        capi.moe_rmsnorm_quantize(None, x.t(), None, g[:4], 1e-6, None, y.t(), None, None)
+    with pytest.raises(capi.MoEError):
+        capi.moe_rmsnorm_quantize(None, x.float(), None, g.float(), 1e-6, None, y.float(), None, None)
+    with pytest.raises(capi.MoEError):
+        capi.moe_rmsnorm_quantize(None, x, None, g, 0.0, None, y, None, None)
