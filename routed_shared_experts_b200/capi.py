@@ -229,70 +229,82 @@ def shared_expert_gate_dot(dtype, x, w, apply_sigmoid, out, stream=None):
 _FLOAT_DT = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_FP16, torch.float32: MOE_DT_F32}
 _OPERAND_DT = {MOE_DT_BF16: (torch.bfloat16,), MOE_DT_FP16: (torch.float16,),
                MOE_DT_FP8_E4M3: (torch.uint8, torch.float8_e4m3fn)}
+_F32, _I32, _BYTES = (torch.float32,), (torch.int32,), (torch.uint8, torch.bool)
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+# The wrappers below are called once per operator of a decode step, whose
+# kernels take a few microseconds: their checks are kept to attribute reads.
 
 
-def _rows(t, name, shape, types):
-    """(address, row stride in elements) of a 2-D tensor whose rows are dense."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must live on a CUDA device")
+def _device(*tensors):
+    """Index of the one device that every tensor lives on, the current one (the
+    calls launch on its stream)."""
+    dev = -1
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d != dev:
+                if dev >= 0 or d < 0:
+                    raise ValueError("tensors must live on one CUDA device")
+                dev = d
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on cuda:{dev}, current device cuda:{torch._C._cuda_getDevice()}")
+    return dev
+
+
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _rows(t, name, rows, cols, types):
+    """Row stride in elements of a [rows, cols] tensor whose rows are dense."""
     if t.dtype not in types:
         raise TypeError(f"{name} has type {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    rows, cols = shape
-    if cols > 1 and t.stride(1) != 1:
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    ld = t.stride(0)
-    return t.data_ptr(), ld if rows > 1 and ld >= cols else _dense_ld(name, t, rows, cols)
-
-
-def _dense_ld(name, t, rows, cols):
-    """Row stride of a tensor with one row or none, whose own says nothing; an
-    expanded or overlapping tensor is refused."""
     if rows > 1:
-        raise ValueError(f"the rows of {name} must not overlap")
-    return -(-cols // 16) * 16
+        if ld < cols:
+            raise ValueError(f"the rows of {name} must not overlap")
+        return ld
+    return -(-cols // 16) * 16  # the stride of one row or none says nothing
 
 
 def _vec(t, name, n, types):
+    """Address of a dense tensor of n elements (None: NULL)."""
     if t is None:
         return None
     if t.dtype not in types:
         raise TypeError(f"{name} has type {t.dtype}")
     if t.numel() != n:
         raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
-    return _ptr(t)
-
-
-def _same_device(first, *others):
-    """The calls launch on the current device's stream: every tensor lives there."""
-    dev = first.device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {dev}, current device {torch.cuda.current_device()}")
-    for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def moe_linear(dtype, x, x_scale, w, w_scale, bias, act, residual, out, stream=None):
     """out = act((x . w^T) * x_scale * w_scale + bias) + residual; x [T,K], w
     [N,K], residual and out [T,N] may be views with any row stride."""
+    types = _OPERAND_DT.get(dtype)
+    if types is None:
+        raise MoEError("moe_linear", -2)
     T, K = x.shape
     N = w.shape[0]
-    if dtype not in _OPERAND_DT:
-        raise MoEError("moe_linear", -2)
-    ops = _OPERAND_DT[dtype]
-    px, ldx = _rows(x, "x", (T, K), ops)
-    pw, ldw = _rows(w, "w", (N, K), ops)
-    po, ldo = _rows(out, "out", (T, N), _FLOAT_DT)
-    pr, ldr = (None, 0) if residual is None else _rows(residual, "residual", (T, N), (out.dtype,))
-    f32 = (torch.float32,)
+    ldx = _rows(x, "x", T, K, types)
+    ldw = _rows(w, "w", N, K, types)
+    ldo = _rows(out, "out", T, N, _FLOAT_DT)
+    ldr = 0 if residual is None else _rows(residual, "residual", T, N, (out.dtype,))
+    dev = _device(x, w, out, residual, bias, x_scale, w_scale)
     ws_rows = 1 if w_scale is None else w_scale.numel()
-    _same_device(x, w, out, residual, bias, x_scale, w_scale)
     _check("moe_linear", lib().moe_linear(
-        dtype, px, ldx, _vec(x_scale, "x_scale", T, f32), pw, ldw, _vec(w_scale, "w_scale", ws_rows, f32), ws_rows,
-        _vec(bias, "bias", N, _FLOAT_DT), MOE_DT_F32 if bias is None else _FLOAT_DT[bias.dtype], act, pr, ldr, po,
-        _FLOAT_DT[out.dtype], ldo, T, N, K, _stream(stream)))
+        dtype, x.data_ptr(), ldx, _vec(x_scale, "x_scale", T, _F32), w.data_ptr(), ldw,
+        _vec(w_scale, "w_scale", ws_rows, _F32), ws_rows, _vec(bias, "bias", N, _FLOAT_DT),
+        MOE_DT_F32 if bias is None else _FLOAT_DT[bias.dtype], act,
+        None if residual is None else residual.data_ptr(), ldr, out.data_ptr(), _FLOAT_DT[out.dtype], ldo, T, N, K,
+        _raw_stream(stream, dev)))
 
 
 def moe_route(logits, bias, expert_mask, num_valid, top_k, score, n_group, topk_group, group_score, renormalize,
@@ -300,28 +312,28 @@ def moe_route(logits, bias, expert_mask, num_valid, top_k, score, n_group, topk_
     """Routing from softmax or sigmoid scores; logits [T,E] may be a view with
     any row stride."""
     T, E = logits.shape
-    pl, ld = _rows(logits, "logits", (T, E), _FLOAT_DT)
-    _same_device(logits, bias, expert_mask, num_valid, topk_ids, topk_weights)
+    ld = _rows(logits, "logits", T, E, _FLOAT_DT)
+    dev = _device(logits, bias, expert_mask, num_valid, topk_ids, topk_weights)
     _check("moe_route", lib().moe_route(
-        pl, _FLOAT_DT[logits.dtype], ld, _vec(bias, "bias", E, (torch.float32,)),
-        _vec(expert_mask, "expert_mask", E, (torch.uint8, torch.bool)),
-        _vec(num_valid, "num_valid", 1, (torch.int32,)), T, E, top_k, score, n_group, topk_group, group_score,
-        int(renormalize), float(routed_scaling_factor), _vec(topk_ids, "topk_ids", T * top_k, (torch.int32,)),
-        _vec(topk_weights, "topk_weights", T * top_k, (torch.float32,)), _stream(stream)))
+        logits.data_ptr(), _FLOAT_DT[logits.dtype], ld, _vec(bias, "bias", E, _F32),
+        _vec(expert_mask, "expert_mask", E, _BYTES), _vec(num_valid, "num_valid", 1, _I32), T, E, top_k, score,
+        n_group, topk_group, group_score, renormalize, routed_scaling_factor,
+        _vec(topk_ids, "topk_ids", T * top_k, _I32), _vec(topk_weights, "topk_weights", T * top_k, _F32),
+        _raw_stream(stream, dev)))
 
 
 def moe_rmsnorm_quantize(quant, x, residual, gamma, eps, residual_out, y, codes, scale, stream=None):
     """z = x + residual -> residual_out; RMS norm of z -> y and / or codes with
     scale. ``quant``: MOE_DT_FP8_E4M3, MOE_DT_MXFP8_E4M3, or None."""
     T, H = x.shape
-    same = (x.dtype,)
-    dtype = _FLOAT_DT.get(x.dtype, MOE_DT_F32)
-    q = MOE_DT_NONE if quant is None else quant
-    mx = q == MOE_DT_MXFP8_E4M3
-    _same_device(x, residual, gamma, residual_out, y, codes, scale)
+    n = T * H
+    xt = x.dtype
+    same = (xt,)
+    mx = quant == MOE_DT_MXFP8_E4M3
+    dev = _device(x, residual, gamma, residual_out, y, codes, scale)
     _check("moe_rmsnorm_quantize", lib().moe_rmsnorm_quantize(
-        dtype, q, _ptr(x), _vec(residual, "residual", T * H, same),
-        _vec(gamma, "gamma", H, (x.dtype, torch.float32)), _FLOAT_DT[gamma.dtype], float(eps), T, H,
-        _vec(residual_out, "residual_out", T * H, same), _vec(y, "y", T * H, same),
-        _vec(codes, "codes", T * H, (torch.uint8, torch.float8_e4m3fn)),
-        _vec(scale, "scale", T * H // 32 if mx else T, (torch.uint8,) if mx else (torch.float32,)), _stream(stream)))
+        _FLOAT_DT.get(xt, MOE_DT_F32), MOE_DT_NONE if quant is None else quant, _vec(x, "x", n, same),
+        _vec(residual, "residual", n, same), _vec(gamma, "gamma", H, (xt, torch.float32)),
+        _FLOAT_DT.get(gamma.dtype, MOE_DT_F32), eps, T, H, _vec(residual_out, "residual_out", n, same),
+        _vec(y, "y", n, same), _vec(codes, "codes", n, _CODES),
+        _vec(scale, "scale", n // 32 if mx else T, (torch.uint8,) if mx else _F32), _raw_stream(stream, dev)))

@@ -18,6 +18,7 @@
 // when N / 128 tiles are fewer than the SMs.
 #pragma once
 #include "gemm.cuh"
+#include "norm.cuh"
 #include "router.cuh"
 
 namespace moe {
@@ -39,7 +40,9 @@ struct LinearArgs {
   void* out;  // rows ldo apart
   size_t ldo;
   int out_dt;  // MOE_DT_BF16, MOE_DT_FP16 or MOE_DT_F32
-  int n_tb;    // token blocks
+  int n_tb;    // token blocks (k_linear_split) or 256-token tiles (k_linear_tile)
+  int tn, n_nt;  // k_linear_tile: outputs per tile (a multiple of 32, at most 256), tiles along N
+  int out_vec, res_vec;  // k_linear_tile: rows allow 16-byte accesses
 };
 
 // Instruction descriptor of kind::f16 with both operands bf16 or both fp16.
@@ -316,6 +319,411 @@ __global__ void __launch_bounds__(kSplitThreads)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, L::kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------ CTA pairs, many tokens
+//
+// k_linear_tile: a 2-CTA cluster per tile of 256 tokens (M, 128 in each CTA)
+// x tn outputs (N, tn / 2 weight rows in each CTA), persistent over the tiles.
+// Warp 0 loads (each CTA its half of both operands), rank 0's warp 1 issues
+// the pair's MMAs, and eight epilogue warps per CTA empty one TMEM accumulator
+// while the MMAs fill the other. tn is chosen by the host so that the tiles
+// fill whole waves of pairs. Each epilogue warp owns 32 token rows and turns
+// its columns, 32 at a time, through 2 KB of shared memory, so that residual
+// reads and result writes are whole 64-byte row segments and no barrier between
+// warps is needed.
+//
+// PROMOTE (fp32 results): the tensor core's accumulation is cut every
+// kPromoteAtoms K atoms and the pieces are added in registers in fp32 (round
+// to nearest), which the accumulator's own additions are not: the error of a
+// sum over K = 7168 drops from about 7e-6 to below 1e-6 of its rms. A 16-bit
+// result's rounding hides that error, so those keep one accumulation.
+
+constexpr int kTileEpiWarps = 8;
+constexpr int kTileThreads = 128 + 32 * kTileEpiWarps;
+constexpr int kPromoteAtoms = 8;
+constexpr int kPromoteTn = 128;  // outputs per tile with PROMOTE: 64 running sums per epilogue thread
+
+struct TileCfg {
+  static constexpr int kStages = 6;
+  static constexpr int kABytes = kTileM * kTileKBytes;
+  static constexpr int kStageBytes = 2 * kABytes;  // A: 128 tokens, B: up to 128 weight rows
+  static constexpr int kStageOut = kStages * kStageBytes;
+  static constexpr int kWarpOut = 2048;  // 32 rows x 64 bytes
+  static constexpr int kVecOffset = kStageOut + kTileEpiWarps * kWarpOut;  // per warp: [scale, bias][4][32]
+  static constexpr int kBarOffset = kVecOffset + kTileEpiWarps * 2 * 4 * 32 * 4;
+  static constexpr int kBytes = kBarOffset + (2 * kStages + 5) * 8 + 16 + 1024;  // + alignment slack
+  static constexpr int kTmemCols = 512;
+  static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
+};
+
+// Byte offset of 16-byte unit u of row r in a warp's 32 x 64-byte staging: the
+// XOR spreads both the row-wise and the row-group-wise accesses over all banks.
+__device__ __forceinline__ int stage_off(int r, int u) { return r * 64 + ((u ^ ((r >> 1) & 3)) << 4); }
+
+// Rows row0.. of a [T, N] matrix, 64 bytes each from column n0 (`cols` valid),
+// to a warp's staging. `vec`: 16-byte accesses are aligned and every column is valid.
+template <typename TE>
+__device__ __forceinline__ void stage_load(uint8_t* st, const TE* src, size_t ld, int row0, int T, int n0, int cols,
+                                           bool vec, int lane) {
+  if (vec) {
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 2);
+      v[i] = row0 + r < T ? *reinterpret_cast<const uint4*>(src + (row0 + r) * ld + n0 + (lane & 3) * (16 / sizeof(TE)))
+                          : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(st + stage_off(i * 8 + (lane >> 2), lane & 3)) = v[i];
+  } else if (lane < cols) {
+    const int b = lane * static_cast<int>(sizeof(TE));
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r)
+      if (row0 + r < T) *reinterpret_cast<TE*>(st + stage_off(r, b >> 4) + (b & 15)) = src[(row0 + r) * ld + n0 + lane];
+  }
+}
+
+template <typename TE>
+__device__ __forceinline__ void stage_store(const uint8_t* st, TE* dst, size_t ld, int row0, int T, int n0, int cols,
+                                            bool vec, int lane) {
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 2);
+      if (row0 + r < T)
+        *reinterpret_cast<uint4*>(dst + (row0 + r) * ld + n0 + (lane & 3) * (16 / sizeof(TE))) =
+            *reinterpret_cast<const uint4*>(st + stage_off(r, lane & 3));
+    }
+  } else if (lane < cols) {
+    const int b = lane * static_cast<int>(sizeof(TE));
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r)
+      if (row0 + r < T) dst[(row0 + r) * ld + n0 + lane] = *reinterpret_cast<const TE*>(st + stage_off(r, b >> 4) + (b & 15));
+  }
+}
+
+template <typename TX>
+__device__ __forceinline__ void unpack_unit(const uint4& v, float* f) {
+  unpack2(v.x, TX(), f[0], f[1]);
+  unpack2(v.y, TX(), f[2], f[3]);
+  unpack2(v.z, TX(), f[4], f[5]);
+  unpack2(v.w, TX(), f[6], f[7]);
+}
+
+// Residual, rounding and store of 32 columns n0.. of this warp's 32 rows
+// (16-bit results): thread = row, through the staging.
+template <typename TX>
+__device__ __forceinline__ void tile_store_16(const LinearArgs& g, uint8_t* st, float (&v)[32], int row0, int n0,
+                                              int lane) {
+  const int cols = min(32, g.N - n0);
+  if (g.residual) {
+    stage_load(st, static_cast<const TX*>(g.residual), g.ldr, row0, g.T, n0, cols, g.res_vec && cols == 32, lane);
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float f[8];
+      unpack_unit<TX>(*reinterpret_cast<const uint4*>(st + stage_off(lane, u)), f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[8 * u + i] += f[i];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    *reinterpret_cast<uint4*>(st + stage_off(lane, u)) =
+        make_uint4(pack2(v[8 * u], v[8 * u + 1], TX()), pack2(v[8 * u + 2], v[8 * u + 3], TX()),
+                   pack2(v[8 * u + 4], v[8 * u + 5], TX()), pack2(v[8 * u + 6], v[8 * u + 7], TX()));
+  __syncwarp();
+  stage_store(st, static_cast<TX*>(g.out), g.ldo, row0, g.T, n0, cols, g.out_vec && cols == 32, lane);
+  __syncwarp();  // the staging is rewritten next
+}
+
+// The same with fp32 results: two halves of 16 columns.
+__device__ __forceinline__ void tile_store_32(const LinearArgs& g, uint8_t* st, float (&v)[32], int row0, int n0,
+                                              int lane) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c0 = n0 + 16 * h;
+    const int cols = min(16, g.N - c0);
+    if (cols <= 0) return;
+    if (g.residual) {
+      stage_load(st, static_cast<const float*>(g.residual), g.ldr, row0, g.T, c0, cols, g.res_vec && cols == 16, lane);
+      __syncwarp();
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float4 f = *reinterpret_cast<const float4*>(st + stage_off(lane, u));
+        v[16 * h + 4 * u] += f.x;
+        v[16 * h + 4 * u + 1] += f.y;
+        v[16 * h + 4 * u + 2] += f.z;
+        v[16 * h + 4 * u + 3] += f.w;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      *reinterpret_cast<float4*>(st + stage_off(lane, u)) =
+          make_float4(v[16 * h + 4 * u], v[16 * h + 4 * u + 1], v[16 * h + 4 * u + 2], v[16 * h + 4 * u + 3]);
+    __syncwarp();
+    stage_store(st, static_cast<float*>(g.out), g.ldo, row0, g.T, c0, cols, g.out_vec && cols == 16, lane);
+    __syncwarp();
+  }
+}
+
+// Token tile and output tile of `tile`: bands of 8 token tiles, tokens fastest,
+// so that the pairs running at one time share operand rows in L2.
+__device__ __forceinline__ void tile_coords(const LinearArgs& g, int tile, int& mt, int& nt) {
+  constexpr int kBand = 8;
+  const int per_band = kBand * g.n_nt;
+  const int band = tile / per_band;
+  const int rows = min(kBand, g.n_tb - band * kBand);
+  const int i = tile - band * per_band;
+  nt = i / rows;
+  mt = band * kBand + (i - nt * rows);
+}
+
+template <bool FP8, bool PROMOTE>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    k_linear_tile(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                  const LinearArgs g) {
+  using L = TileCfg;
+  constexpr int KE = FP8 ? 128 : 64;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOffset);
+  uint64_t* empty = full + L::kStages;
+  uint64_t* acc_full = empty + L::kStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&acc_full[a], 1);
+      mbar_init(&acc_empty[a], 2 * kTileEpiWarps);  // every epilogue warp of both CTAs
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, L::kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers initialised before any remote use
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  const int total = g.n_tb * g.n_nt;
+  const int unit0 = static_cast<int>(blockIdx.x >> 1);
+  const int n_units = static_cast<int>(gridDim.x >> 1);
+  const int n_kc = PROMOTE ? (g.nk + kPromoteAtoms - 1) / kPromoteAtoms : 1;  // accumulations per tile
+  const int kc_atoms = PROMOTE ? kPromoteAtoms : g.nk;
+  const int b_rows = g.tn / 2;  // weight rows in each CTA
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol = policy_evict_last();  // both operands are read by several tiles
+      const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+      const uint32_t bytes = static_cast<uint32_t>(L::kABytes + b_rows * kTileKBytes);
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t pending = 0, parity = 0;
+      bool ok = true;
+      for (int tile = unit0; tile < total && ok; tile += n_units) {
+        int mt, nt;
+        tile_coords(g, tile, mt, nt);
+        const int x_row = mt * 2 * kTileM + static_cast<int>(rank) * kTileM;
+        const int w_row = nt * g.tn + static_cast<int>(rank) * b_rows;
+        for (int k = 0; k < g.nk; ++k) {
+          ok = mbar_wait(&empty[stage], phase ^ 1u, abort_flag);
+          if (!ok) break;
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * bytes);  // the bytes of both CTAs
+          uint8_t* a = smem + stage * L::kStageBytes;
+          const uint32_t fb = full0 + 8u * static_cast<uint32_t>(stage);
+          tma_load_2d_pair(a, &tmX, fb, k * KE, x_row, pol);
+          tma_load_2d_pair(a + L::kABytes, &tmW, fb, k * KE, w_row, pol);
+          pending |= 1u << stage;
+          parity = (parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == L::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        if (rank == 0) {
+          for (int s = 0; s < L::kStages; ++s)
+            if ((pending >> s) & 1u) drain_wait(&full[s], (parity >> s) & 1u);
+        } else if (pending) {
+          // rank 1's copies complete on rank 0's barriers, which it cannot wait
+          // on: give copies in flight a bounded 2 ms to land before unwinding
+          const uint64_t t0 = globaltimer();
+          while (globaltimer() - t0 < 2000000ull) __nanosleep(1000);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      const uint32_t idesc = FP8 ? idesc_e4m3(2 * kTileM, g.tn) : idesc_16bit(2 * kTileM, g.tn, g.f16);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      int j = 0;  // accumulation counter: accumulator j % 2
+      for (int tile = unit0; tile < total && ok; tile += n_units) {
+        for (int kc = 0; kc < n_kc && ok; ++kc, ++j) {
+          const int acc = j & 1;
+          ok = mbar_wait(&acc_empty[acc], ((static_cast<uint32_t>(j) >> 1) & 1u) ^ 1u, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
+          const int k_lo = kc * kc_atoms, k_hi = min(g.nk, k_lo + kc_atoms);
+          for (int k = k_lo; k < k_hi; ++k) {
+            ok = mbar_wait(&full[stage], phase, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t a_addr = smem_u32(smem + stage * L::kStageBytes);
+            const uint64_t adesc = sw128_kmajor_desc(a_addr);
+            const uint64_t bdesc = sw128_kmajor_desc(a_addr + L::kABytes);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint32_t accum = (k != k_lo || kk != 0) ? 1u : 0u;
+              if (FP8) umma_f8_pair(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, idesc, accum);
+              else umma_f16_pair(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, idesc, accum);
+            }
+            umma_commit_pair_multicast(&empty[stage], 3);
+            if (++stage == L::kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+          if (ok) umma_commit_pair_multicast(&acc_full[acc], 3);
+        }
+      }
+      if (!ok) {
+        umma_commit_pair(mapa_shared(smem_u32(drain), 0));
+        drain_wait(drain, 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    const int ew = warp - 4;
+    const int q = ew & 3;     // TMEM lane quarter
+    const int half = ew >> 2;  // columns 32 c.. with c % 2 == half
+    uint8_t* st = smem + L::kStageOut + ew * L::kWarpOut;
+    float* ws_sm = reinterpret_cast<float*>(smem + L::kVecOffset) + ew * 256;  // this warp's columns, by chunk
+    float* b_sm = ws_sm + 128;
+    const uint32_t acc_empty0 = mapa_shared(smem_u32(acc_empty), 0);
+    const int chunks = g.tn / 32;
+    int j = 0;
+    bool ok = true;
+    for (int tile = unit0; tile < total && ok; tile += n_units) {
+      int mt, nt;
+      tile_coords(g, tile, mt, nt);
+      const int row0 = mt * 2 * kTileM + static_cast<int>(rank) * kTileM + 32 * q;
+      const int t = row0 + lane;
+      // weight scales and bias of this warp's columns, fetched while the sum is being built
+      for (int c = half; c < chunks; c += 2) {
+        const int n = nt * g.tn + 32 * c + lane;
+        ws_sm[16 * (c - half) + lane] = FP8 && n < g.N ? __ldg(g.w_scale + static_cast<size_t>(n) * g.w_scale_step) : 1.f;
+        b_sm[16 * (c - half) + lane] = g.bias && n < g.N ? load_typed(g.bias, g.bias_dt, n) : 0.f;
+      }
+      const float xs = g.x_scale && t < g.T ? __ldg(g.x_scale + t) : 1.f;
+      __syncwarp();
+      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+
+      auto finish = [&](float (&v)[32], int c) {
+        const int n0 = nt * g.tn + 32 * c;
+        if (row0 >= g.T || n0 >= g.N) return;
+        const float4* ws4 = reinterpret_cast<const float4*>(ws_sm + 16 * (c - half));
+        const float4* b4 = reinterpret_cast<const float4*>(b_sm + 16 * (c - half));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (FP8) {
+            const float4 w = ws4[i];
+            v[4 * i] *= xs * w.x;
+            v[4 * i + 1] *= xs * w.y;
+            v[4 * i + 2] *= xs * w.z;
+            v[4 * i + 3] *= xs * w.w;
+          }
+          const float4 b = b4[i];
+          v[4 * i] += b.x;
+          v[4 * i + 1] += b.y;
+          v[4 * i + 2] += b.z;
+          v[4 * i + 3] += b.w;
+        }
+        apply_act(v, g.act);
+        if (PROMOTE) tile_store_32(g, st, v, row0, n0, lane);
+        else if (g.out_dt == 0) tile_store_16<__nv_bfloat16>(g, st, v, row0, n0, lane);
+        else tile_store_16<__half>(g, st, v, row0, n0, lane);
+      };
+      auto release = [&](int acc) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acc_empty0 + 8u * static_cast<uint32_t>(acc));
+      };
+
+      if constexpr (PROMOTE) {
+        float sum[kPromoteTn / 64][32];
+        for (int kc = 0; kc < n_kc; ++kc, ++j) {
+          const int acc = j & 1;
+          ok = mbar_wait(&acc_full[acc], (static_cast<uint32_t>(j) >> 1) & 1u, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < kPromoteTn / 64; ++i) {
+            const int c = 2 * i + half;
+            if (c < chunks) {
+              float v[32];
+              tmem_ld32(t_row + static_cast<uint32_t>(acc * 256 + 32 * c), v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) sum[i][e] = kc == 0 ? v[e] : sum[i][e] + v[e];
+            }
+          }
+          release(acc);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < kPromoteTn / 64; ++i)
+          if (2 * i + half < chunks) finish(sum[i], 2 * i + half);
+      } else {
+        const int acc = j & 1;
+        ok = mbar_wait(&acc_full[acc], (static_cast<uint32_t>(j) >> 1) & 1u, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        for (int c = half; c < chunks; c += 2) {
+          float v[32];
+          tmem_ld32(t_row + static_cast<uint32_t>(acc * 256 + 32 * c), v);
+          tmem_wait_ld();
+          if (c + 2 >= chunks) release(acc);
+          finish(v, c);
+        }
+        if (half >= chunks) release(acc);  // one-chunk tiles: the second half of the warps reads nothing
+        ++j;
+      }
+      __syncwarp();  // the scales and bias are rewritten next
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // no CTA leaves while its peer may still signal its barriers
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, L::kTmemCols);
   }
 }
 

@@ -465,19 +465,84 @@ moe_status_t launch_linear_split(const LinearCall& c, int S, cudaStream_t s) {
   return MOE_OK;
 }
 
+template <bool FP8, bool PROMOTE>
+moe_status_t launch_linear_tile(const LinearCall& c, int tn, cudaStream_t s) {
+  using L = moe::TileCfg;
+  CUtensorMap tx, tw;
+  moe_status_t r = make_linear_map(&tx, c.dtype, c.x, c.g.T, c.K, c.ldx, moe::kTileM);
+  if (r != MOE_OK) return r;
+  r = make_linear_map(&tw, c.dtype, c.w, c.g.N, c.K, c.ldw, tn / 2);
+  if (r != MOE_OK) return r;
+  auto kern = moe::k_linear_tile<FP8, PROMOTE>;
+  static std::atomic<int> attr_set[64];
+  r = set_smem_attr(kern, L::kBytes, attr_set);
+  if (r != MOE_OK) return r;
+  moe::LinearArgs g = c.g;
+  g.tn = tn;
+  g.n_tb = (g.T + 2 * moe::kTileM - 1) / (2 * moe::kTileM);
+  g.n_nt = (g.N + tn - 1) / tn;
+  const int64_t tiles = static_cast<int64_t>(g.n_tb) * g.n_nt;
+  if (tiles > INT32_MAX / 2) return MOE_ERR_SHAPE;
+  const int os = float_size(g.out_dt);
+  g.out_vec = aligned16(g.out) && g.ldo * os % 16 == 0;
+  g.res_vec = g.residual && aligned16(g.residual) && g.ldr * os % 16 == 0;
+  const int pairs = num_sms() / 2;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
+  cfg.blockDim = dim3(moe::kTileThreads);
+  cfg.dynamicSmemBytes = L::kBytes;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  MOE_CK(cudaLaunchKernelEx(&cfg, kern, tx, tw, g));
+  return MOE_OK;
+}
+
+struct LinearPlan {
+  int bn, split;  // k_linear_split: tokens per tile, CTAs along K
+  int tn;         // k_linear_tile: outputs per tile, or 0
+};
+
+LinearPlan plan_linear(int T, int N, int nk, bool f32_out) {
+  LinearPlan p{};
+  if (T > 256) {
+    const int64_t tb = (T + 255) / 256;
+    const int pairs = num_sms() / 2;
+    int64_t best = INT64_MAX;
+    for (int tn = f32_out ? moe::kPromoteTn : 256; tn >= 64; tn -= 32) {
+      const int64_t waves = (tb * ((N + tn - 1) / tn) + pairs - 1) / pairs;
+      const int64_t cost = waves * (static_cast<int64_t>(nk) * (tn > 128 ? 2 * tn : 200 + tn) + 3000);
+      if (cost < best) {
+        best = cost;
+        p.tn = tn;
+      }
+    }
+    return p;
+  }
+  p.bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
+  const int64_t tiles = static_cast<int64_t>((N + 127) / 128) * ((T + p.bn - 1) / p.bn);
+  p.split = 8;
+  while (p.split > 1 && (tiles * p.split > num_sms() || nk < 4 * p.split)) p.split /= 2;
+  return p;
+}
+
 template <bool FP8>
 moe_status_t launch_linear(const LinearCall& c, cudaStream_t s) {
-  const int bn = c.g.T <= 16 ? 16 : c.g.T <= 32 ? 32 : c.g.T <= 64 ? 64 : c.g.T <= 128 ? 128 : 256;
-  const int64_t tiles = static_cast<int64_t>((c.g.N + 127) / 128) * ((c.g.T + bn - 1) / bn);
-  int S = 8;
-  while (S > 1 && (tiles * S > num_sms() || c.g.nk < 4 * S)) S /= 2;
-  switch (bn) {
-    case 16: return launch_linear_split<16, FP8>(c, S, s);
-    case 32: return launch_linear_split<32, FP8>(c, S, s);
-    case 64: return launch_linear_split<64, FP8>(c, S, s);
-    case 128: return launch_linear_split<128, FP8>(c, S, s);
+  const bool f32 = c.g.out_dt == MOE_DT_F32;
+  const LinearPlan p = plan_linear(c.g.T, c.g.N, c.g.nk, f32);
+  if (p.tn) return f32 ? launch_linear_tile<FP8, true>(c, p.tn, s) : launch_linear_tile<FP8, false>(c, p.tn, s);
+  switch (p.bn) {
+    case 16: return launch_linear_split<16, FP8>(c, p.split, s);
+    case 32: return launch_linear_split<32, FP8>(c, p.split, s);
+    case 64: return launch_linear_split<64, FP8>(c, p.split, s);
+    case 128: return launch_linear_split<128, FP8>(c, p.split, s);
   }
-  return launch_linear_split<256, FP8>(c, S, s);
+  return launch_linear_split<256, FP8>(c, p.split, s);
 }
 
 template <int VPL>
