@@ -7,6 +7,14 @@
 // runs), the sum is kept in fp32 in TMEM, everything after it happens in
 // registers, and the result is rounded once.
 //
+// A pipeline stage holds kLinAtoms K atoms, and two producer warps load one
+// operand each, with one copy per stage: the map views the operand as
+// [atoms][rows][128 bytes], so that a box of several atoms lands as whole
+// swizzled tiles one after another. With one atom per stage and one producer
+// each role's fixed cost per stage (barrier wait, arrival, copy issue, commit)
+// set the pace, 0.3 us per atom whatever its bytes. The last stage, where K
+// ends inside it, is loaded atom by atom through a plain 2D map.
+//
 // k_linear_split: weights on the MMA's M side (128 outputs per tile), up to BN
 // tokens on N, and the K axis split over the S CTAs of a cluster. Each CTA
 // leaves its fp32 partial tile in its own shared memory; after a cluster
@@ -25,9 +33,12 @@ namespace moe {
 
 enum LinearAct : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4, kActSigmoid = 5 };
 
+constexpr int kLinAtoms = 2;  // K atoms per pipeline stage
+
 struct LinearArgs {
   int T, N;
   int nk;                // K atoms
+  int nk_full;           // of those, atoms that K fills
   int f16;               // 16-bit operands are fp16
   const float* x_scale;  // [T] or nullptr (8-bit operands)
   const float* w_scale;  // [N], or one value with w_scale_step = 0
@@ -108,16 +119,39 @@ __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr) {
   return v;
 }
 
+// Copies of stage `ks` of one operand: rows row0.. into consecutive tiles of
+// `atom_bytes`. `tm`: the [atoms][rows][128 bytes] map, `tail`: the 2D map.
+template <int KE, bool PAIR>
+__device__ __forceinline__ void load_stage(uint8_t* dst, const CUtensorMap* tm, const CUtensorMap* tail, uint64_t* bar,
+                                           uint32_t bar_cluster, int ks, int row0, int atom_bytes, const LinearArgs& g,
+                                           uint64_t policy) {
+  const int k0 = ks * kLinAtoms;
+  if (k0 + kLinAtoms <= g.nk_full) {
+    if constexpr (PAIR) tma_load_3d_pair(dst, tm, bar_cluster, 0, row0, k0, policy);
+    else tma_load_3d(dst, tm, bar, 0, row0, k0, policy);
+  } else {
+#pragma unroll
+    for (int a = 0; a < kLinAtoms; ++a) {
+      if (k0 + a < g.nk) {
+        if constexpr (PAIR) tma_load_2d_pair(dst + a * atom_bytes, tail, bar_cluster, (k0 + a) * KE, row0, policy);
+        else tma_load_2d(dst + a * atom_bytes, tail, bar, (k0 + a) * KE, row0, policy);
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------ K split over a cluster
 
-constexpr int kSplitThreads = 192;  // producer, MMA, four epilogue warps
+constexpr int kSplitThreads = 224;  // weight producer, MMA, token producer, four epilogue warps
 
 template <int BN>
 struct SplitCfg {
-  static constexpr int kStageBytes = (kTileM + BN) * kTileKBytes;
+  static constexpr int kAtomW = kTileM * kTileKBytes;
+  static constexpr int kAtomX = BN * kTileKBytes;
+  static constexpr int kStageBytes = (kAtomW + kAtomX) * kLinAtoms;
   // about 100 KB of operands in flight per CTA up to 64 tokens (two CTAs per
   // SM), all of shared memory above
-  static constexpr int kStages = BN == 16 ? 5 : BN == 32 ? 5 : BN == 64 ? 4 : BN == 128 ? 6 : 4;
+  static constexpr int kStages = BN == 16 ? 3 : BN == 32 ? 2 : BN == 64 ? 2 : BN == 128 ? 3 : 2;
   static constexpr int kBarOffset = kStages * kStageBytes;
   static constexpr int kBytes = kBarOffset + (2 * kStages + 2) * 8 + 16 + 1024;  // + alignment slack
   static constexpr int kTmemCols = BN < 32 ? 32 : BN;
@@ -152,7 +186,8 @@ __device__ __forceinline__ void split_finish(const LinearArgs& g, float (&v)[C],
 
 template <int BN, bool FP8>
 __global__ void __launch_bounds__(kSplitThreads)
-    k_linear_split(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+    k_linear_split(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWt,
+                   const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXt,
                    const LinearArgs g, int S) {
   using L = SplitCfg<BN>;
   constexpr int KE = FP8 ? 128 : 64;  // K elements per atom
@@ -171,12 +206,13 @@ __global__ void __launch_bounds__(kSplitThreads)
   const int tile = static_cast<int>(blockIdx.x) / S;
   const int nt = tile / g.n_tb;
   const int t_base = (tile - nt * g.n_tb) * BN;
-  const int k0 = static_cast<int>(static_cast<long long>(g.nk) * rank / S);
-  const int k1 = static_cast<int>(static_cast<long long>(g.nk) * (rank + 1) / S);
+  const int ns = (g.nk + kLinAtoms - 1) / kLinAtoms;  // stages along K; this CTA's are s0 .. s1 - 1
+  const int s0 = static_cast<int>(static_cast<long long>(ns) * rank / S);
+  const int s1 = static_cast<int>(static_cast<long long>(ns) * (rank + 1) / S);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);  // each producer arms it with its own bytes
       mbar_init(&empty[s], 1);
     }
     mbar_init(done, 1);
@@ -193,22 +229,27 @@ __global__ void __launch_bounds__(kSplitThreads)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 2) {
     if (lane == 0) {
+      const bool is_w = warp == 0;
+      const CUtensorMap* tm = is_w ? &tmW : &tmX;
+      const CUtensorMap* tail = is_w ? &tmWt : &tmXt;
       // weights pass once through L2 when one token block reads them
-      const uint64_t pol_w = g.n_tb == 1 ? policy_evict_first() : policy_evict_last();
-      const uint64_t pol_x = policy_evict_last();
+      const uint64_t pol = is_w && g.n_tb == 1 ? policy_evict_first() : policy_evict_last();
+      const int row0 = is_w ? nt * kTileM : t_base;
+      const int atom_bytes = is_w ? L::kAtomW : L::kAtomX;
+      const int off = is_w ? 0 : L::kAtomW * kLinAtoms;
       int stage = 0;
       uint32_t phase = 0;
       uint32_t pending = 0, parity = 0;  // stages armed and not re-acquired, for the drain
       bool ok = true;
-      for (int k = k0; k < k1; ++k) {
+      for (int ks = s0; ks < s1; ++ks) {
         ok = mbar_wait(&empty[stage], phase ^ 1u, abort_flag);
         if (!ok) break;
-        uint8_t* a = smem + stage * L::kStageBytes;
-        mbar_arrive_expect_tx(&full[stage], L::kStageBytes);
-        tma_load_2d(a, &tmW, &full[stage], k * KE, nt * kTileM, pol_w);
-        tma_load_2d(a + kTileM * kTileKBytes, &tmX, &full[stage], k * KE, t_base, pol_x);
+        const int na = min(kLinAtoms, g.nk - ks * kLinAtoms);
+        mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(na * atom_bytes));
+        load_stage<KE, false>(smem + stage * L::kStageBytes + off, tm, tail, &full[stage], 0, ks, row0, atom_bytes, g,
+                              pol);
         pending |= 1u << stage;
         parity = (parity & ~(1u << stage)) | (phase << stage);
         if (++stage == L::kStages) {
@@ -228,18 +269,24 @@ __global__ void __launch_bounds__(kSplitThreads)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int k = k0; k < k1; ++k) {
+      for (int ks = s0; ks < s1; ++ks) {
         ok = mbar_wait(&full[stage], phase, abort_flag);
         if (!ok) break;
         tc_fence_after();
+        const int na = min(kLinAtoms, g.nk - ks * kLinAtoms);
         const uint32_t a_addr = smem_u32(smem + stage * L::kStageBytes);
-        const uint64_t adesc = sw128_kmajor_desc(a_addr);
-        const uint64_t bdesc = sw128_kmajor_desc(a_addr + kTileM * kTileKBytes);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {  // 32 K-bytes per MMA: +2 in the (addr >> 4) field
-          const uint32_t accum = (k != k0 || kk != 0) ? 1u : 0u;
-          if (FP8) umma_f8(tmem_base, adesc + 2 * kk, bdesc + 2 * kk, idesc, accum);
-          else umma_f16(tmem_base, adesc + 2 * kk, bdesc + 2 * kk, idesc, accum);
+        for (int a = 0; a < kLinAtoms; ++a) {
+          if (a < na) {
+            const uint64_t adesc = sw128_kmajor_desc(a_addr + a * L::kAtomW);
+            const uint64_t bdesc = sw128_kmajor_desc(a_addr + L::kAtomW * kLinAtoms + a * L::kAtomX);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {  // 32 K-bytes per MMA: +2 in the (addr >> 4) field
+              const uint32_t accum = (ks != s0 || (a | kk) != 0) ? 1u : 0u;
+              if (FP8) umma_f8(tmem_base, adesc + 2 * kk, bdesc + 2 * kk, idesc, accum);
+              else umma_f16(tmem_base, adesc + 2 * kk, bdesc + 2 * kk, idesc, accum);
+            }
+          }
         }
         umma_commit(&empty[stage]);
         if (++stage == L::kStages) {
@@ -263,7 +310,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   const int nv = min(BN, g.T - t_base);  // tokens of this block
   float ws = 0.f, bias = 0.f;
   bool ok = false;
-  if (warp >= 2) {
+  if (warp >= 3) {
     if (n < g.N) {  // fetched while the sum is still being built
       if (g.x_scale) ws = __ldg(g.w_scale + static_cast<size_t>(n) * g.w_scale_step);
       if (g.bias) bias = load_typed(g.bias, g.bias_dt, n);
@@ -274,7 +321,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   }
   const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
   if (S == 1) {
-    if (warp >= 2 && __all_sync(0xffffffffu, ok)) {
+    if (warp >= 3 && __all_sync(0xffffffffu, ok)) {
       for (int c0 = 0; c0 < nv; c0 += 16) {
         float v[16];
         tmem_ld16(t_row + static_cast<uint32_t>(c0), v);
@@ -285,7 +332,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   } else {
     // the stages are free: every copy has landed and every MMA has read them
     float* part = reinterpret_cast<float*>(smem);  // [token column][128 outputs]
-    if (warp >= 2 && __all_sync(0xffffffffu, ok)) {
+    if (warp >= 3 && __all_sync(0xffffffffu, ok)) {
       for (int c0 = 0; c0 < nv; c0 += 16) {
         float v[16];
         tmem_ld16(t_row + static_cast<uint32_t>(c0), v);
@@ -295,7 +342,7 @@ __global__ void __launch_bounds__(kSplitThreads)
       }
     }
     cluster_sync_all();
-    if (warp >= 2) {
+    if (warp >= 3) {
       constexpr int C = 4;
       const int c_lo = nv * rank / S, c_hi = nv * (rank + 1) / S;
       const uint32_t part0 = smem_u32(part) + 4u * static_cast<uint32_t>(rowi);
@@ -312,7 +359,7 @@ __global__ void __launch_bounds__(kSplitThreads)
         if (n < g.N) split_finish<C>(g, v, n, t_base + c0, t_base + c_hi, ws, bias);
       }
     }
-    cluster_sync_all();  // no CTA leaves while a peer may still read its partial tile
+    cluster_sync_relaxed();  // no CTA leaves while a peer may still read its partial tile
   }
   tc_fence_before();
   __syncthreads();
@@ -346,9 +393,10 @@ constexpr int kPromoteAtoms = 8;
 constexpr int kPromoteTn = 128;  // outputs per tile with PROMOTE: 64 running sums per epilogue thread
 
 struct TileCfg {
-  static constexpr int kStages = 6;
-  static constexpr int kABytes = kTileM * kTileKBytes;
-  static constexpr int kStageBytes = 2 * kABytes;  // A: 128 tokens, B: up to 128 weight rows
+  static constexpr int kStages = 3;
+  static constexpr int kAtom = kTileM * kTileKBytes;
+  static constexpr int kABytes = kAtom * kLinAtoms;  // 128 tokens
+  static constexpr int kStageBytes = 2 * kABytes;    // then up to 128 weight rows
   static constexpr int kStageOut = kStages * kStageBytes;
   static constexpr int kWarpOut = 2048;  // 32 rows x 64 bytes
   static constexpr int kVecOffset = kStageOut + kTileEpiWarps * kWarpOut;  // per warp: [scale, bias][4][32]
@@ -483,7 +531,8 @@ __device__ __forceinline__ void tile_coords(const LinearArgs& g, int tile, int& 
 
 template <bool FP8, bool PROMOTE>
 __global__ void __launch_bounds__(kTileThreads, 1)
-    k_linear_tile(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+    k_linear_tile(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXt,
+                  const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWt,
                   const LinearArgs g) {
   using L = TileCfg;
   constexpr int KE = FP8 ? 128 : 64;
@@ -502,7 +551,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const uint32_t rank = cluster_ctarank();
   if (threadIdx.x == 0) {
     for (int s = 0; s < L::kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);  // armed by rank 0's two producers with both CTAs' bytes
       mbar_init(&empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -526,15 +575,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int total = g.n_tb * g.n_nt;
   const int unit0 = static_cast<int>(blockIdx.x >> 1);
   const int n_units = static_cast<int>(gridDim.x >> 1);
-  const int n_kc = PROMOTE ? (g.nk + kPromoteAtoms - 1) / kPromoteAtoms : 1;  // accumulations per tile
-  const int kc_atoms = PROMOTE ? kPromoteAtoms : g.nk;
+  const int ns = (g.nk + kLinAtoms - 1) / kLinAtoms;  // stages per tile
+  const int kc_stages = PROMOTE ? kPromoteAtoms / kLinAtoms : ns;
+  const int n_kc = PROMOTE ? (ns + kc_stages - 1) / kc_stages : 1;  // accumulations per tile
   const int b_rows = g.tn / 2;  // weight rows in each CTA
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 2) {
     if (lane == 0) {
+      const bool is_x = warp == 0;
+      const CUtensorMap* tm = is_x ? &tmX : &tmW;
+      const CUtensorMap* tail = is_x ? &tmXt : &tmWt;
       const uint64_t pol = policy_evict_last();  // both operands are read by several tiles
       const uint32_t full0 = mapa_shared(smem_u32(full), 0);
-      const uint32_t bytes = static_cast<uint32_t>(L::kABytes + b_rows * kTileKBytes);
+      const int atom_bytes = is_x ? L::kAtom : b_rows * kTileKBytes;
+      const int off = is_x ? 0 : L::kABytes;
       int stage = 0;
       uint32_t phase = 0;
       uint32_t pending = 0, parity = 0;
@@ -542,16 +596,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (int tile = unit0; tile < total && ok; tile += n_units) {
         int mt, nt;
         tile_coords(g, tile, mt, nt);
-        const int x_row = mt * 2 * kTileM + static_cast<int>(rank) * kTileM;
-        const int w_row = nt * g.tn + static_cast<int>(rank) * b_rows;
-        for (int k = 0; k < g.nk; ++k) {
+        const int row0 = is_x ? mt * 2 * kTileM + static_cast<int>(rank) * kTileM
+                              : nt * g.tn + static_cast<int>(rank) * b_rows;
+        for (int ks = 0; ks < ns; ++ks) {
           ok = mbar_wait(&empty[stage], phase ^ 1u, abort_flag);
           if (!ok) break;
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * bytes);  // the bytes of both CTAs
-          uint8_t* a = smem + stage * L::kStageBytes;
-          const uint32_t fb = full0 + 8u * static_cast<uint32_t>(stage);
-          tma_load_2d_pair(a, &tmX, fb, k * KE, x_row, pol);
-          tma_load_2d_pair(a + L::kABytes, &tmW, fb, k * KE, w_row, pol);
+          const int na = min(kLinAtoms, g.nk - ks * kLinAtoms);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(2 * na * atom_bytes));
+          load_stage<KE, true>(smem + stage * L::kStageBytes + off, tm, tail, nullptr,
+                               full0 + 8u * static_cast<uint32_t>(stage), ks, row0, atom_bytes, g, pol);
           pending |= 1u << stage;
           parity = (parity & ~(1u << stage)) | (phase << stage);
           if (++stage == L::kStages) {
@@ -587,19 +640,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (!ok) break;
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
-          const int k_lo = kc * kc_atoms, k_hi = min(g.nk, k_lo + kc_atoms);
-          for (int k = k_lo; k < k_hi; ++k) {
+          const int s_lo = kc * kc_stages, s_hi = min(ns, s_lo + kc_stages);
+          for (int ks = s_lo; ks < s_hi; ++ks) {
             ok = mbar_wait(&full[stage], phase, abort_flag);
             if (!ok) break;
             tc_fence_after();
+            const int na = min(kLinAtoms, g.nk - ks * kLinAtoms);
             const uint32_t a_addr = smem_u32(smem + stage * L::kStageBytes);
-            const uint64_t adesc = sw128_kmajor_desc(a_addr);
-            const uint64_t bdesc = sw128_kmajor_desc(a_addr + L::kABytes);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint32_t accum = (k != k_lo || kk != 0) ? 1u : 0u;
-              if (FP8) umma_f8_pair(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, idesc, accum);
-              else umma_f16_pair(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, idesc, accum);
+            for (int a = 0; a < kLinAtoms; ++a) {
+              if (a < na) {
+                const uint64_t adesc = sw128_kmajor_desc(a_addr + a * L::kAtom);
+                const uint64_t bdesc = sw128_kmajor_desc(a_addr + L::kABytes + a * b_rows * kTileKBytes);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                  const uint32_t accum = (ks != s_lo || (a | kk) != 0) ? 1u : 0u;
+                  if (FP8) umma_f8_pair(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, idesc, accum);
+                  else umma_f16_pair(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, idesc, accum);
+                }
+              }
             }
             umma_commit_pair_multicast(&empty[stage], 3);
             if (++stage == L::kStages) {
@@ -670,7 +729,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       auto release = [&](int acc) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(acc_empty0 + 8u * static_cast<uint32_t>(acc));
+        // relaxed: the TMEM reads are complete, and the result stores of earlier chunks need not land first
+        if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty0 + 8u * static_cast<uint32_t>(acc));
       };
 
       if constexpr (PROMOTE) {
@@ -720,7 +780,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // no CTA leaves while its peer may still signal its barriers
+  cluster_sync_relaxed();  // no CTA leaves while its peer may still signal its barriers
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, L::kTmemCols);

@@ -411,17 +411,31 @@ inline bool is_float_dt(int dtype) { return is_16bit(dtype) || dtype == MOE_DT_F
 inline int float_size(int dtype) { return dtype == MOE_DT_F32 ? 4 : 2; }
 inline bool aligned_to(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-// 2D operand of the linear product: `rows` rows of K elements, ld elements
-// apart, read in boxes of one 128-byte K atom x box_rows.
-moe_status_t make_linear_map(CUtensorMap* m, int dtype, const void* base, int rows, int K, int64_t ld, int box_rows) {
+// An operand of the linear product, `rows` rows of K elements, ld elements
+// apart: `m` as [atoms][rows][128 bytes] over the K atoms that K fills, read
+// kLinAtoms atoms x box_rows rows at a time, and `tail` as the plain matrix,
+// read one atom at a time (zeros past K). No whole atom: `m` is not read.
+moe_status_t make_linear_maps(CUtensorMap* m, CUtensorMap* tail, int dtype, const void* base, int rows, int K,
+                              int64_t ld, int box_rows) {
   const int es = is_16bit(dtype) ? 2 : 1;
   const CUtensorMapDataType dt = dtype == MOE_DT_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                  : dtype == MOE_DT_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                         : CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t st[1] = {static_cast<cuuint64_t>(ld) * es};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(moe::kTileKBytes / es), static_cast<cuuint32_t>(box_rows)};
-  return make_map(m, dt, 2, base, dims, st, box);
+  const cuuint32_t ke = static_cast<cuuint32_t>(moe::kTileKBytes / es);
+  const cuuint64_t row = static_cast<cuuint64_t>(ld) * es;
+  const cuuint64_t dims2[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t st2[1] = {row};
+  const cuuint32_t box2[2] = {ke, static_cast<cuuint32_t>(box_rows)};
+  const moe_status_t r = make_map(tail, dt, 2, base, dims2, st2, box2);
+  if (r != MOE_OK) return r;
+  if (K / ke < moe::kLinAtoms) {
+    *m = *tail;
+    return MOE_OK;
+  }
+  const cuuint64_t dims3[3] = {ke, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(K / ke)};
+  const cuuint64_t st3[2] = {row, moe::kTileKBytes};
+  const cuuint32_t box3[3] = {ke, static_cast<cuuint32_t>(box_rows), moe::kLinAtoms};
+  return make_map(m, dt, 3, base, dims3, st3, box3);
 }
 
 struct LinearCall {
@@ -436,10 +450,10 @@ template <int BN, bool FP8>
 moe_status_t launch_linear_split(const LinearCall& c, int S, cudaStream_t s) {
   using L = moe::SplitCfg<BN>;
   static_assert(L::kBytes <= 227 * 1024, "shared memory per CTA");
-  CUtensorMap tw, tx;
-  moe_status_t r = make_linear_map(&tw, c.dtype, c.w, c.g.N, c.K, c.ldw, moe::kTileM);
+  CUtensorMap tw, twt, tx, txt;
+  moe_status_t r = make_linear_maps(&tw, &twt, c.dtype, c.w, c.g.N, c.K, c.ldw, moe::kTileM);
   if (r != MOE_OK) return r;
-  r = make_linear_map(&tx, c.dtype, c.x, c.g.T, c.K, c.ldx, BN);
+  r = make_linear_maps(&tx, &txt, c.dtype, c.x, c.g.T, c.K, c.ldx, BN);
   if (r != MOE_OK) return r;
   auto kern = moe::k_linear_split<BN, FP8>;
   static std::atomic<int> attr_set[64];
@@ -461,17 +475,17 @@ moe_status_t launch_linear_split(const LinearCall& c, int S, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  MOE_CK(cudaLaunchKernelEx(&cfg, kern, tw, tx, g, S));
+  MOE_CK(cudaLaunchKernelEx(&cfg, kern, tw, twt, tx, txt, g, S));
   return MOE_OK;
 }
 
 template <bool FP8, bool PROMOTE>
 moe_status_t launch_linear_tile(const LinearCall& c, int tn, cudaStream_t s) {
   using L = moe::TileCfg;
-  CUtensorMap tx, tw;
-  moe_status_t r = make_linear_map(&tx, c.dtype, c.x, c.g.T, c.K, c.ldx, moe::kTileM);
+  CUtensorMap tx, txt, tw, twt;
+  moe_status_t r = make_linear_maps(&tx, &txt, c.dtype, c.x, c.g.T, c.K, c.ldx, moe::kTileM);
   if (r != MOE_OK) return r;
-  r = make_linear_map(&tw, c.dtype, c.w, c.g.N, c.K, c.ldw, tn / 2);
+  r = make_linear_maps(&tw, &twt, c.dtype, c.w, c.g.N, c.K, c.ldw, tn / 2);
   if (r != MOE_OK) return r;
   auto kern = moe::k_linear_tile<FP8, PROMOTE>;
   static std::atomic<int> attr_set[64];
@@ -499,7 +513,7 @@ moe_status_t launch_linear_tile(const LinearCall& c, int tn, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  MOE_CK(cudaLaunchKernelEx(&cfg, kern, tx, tw, g));
+  MOE_CK(cudaLaunchKernelEx(&cfg, kern, tx, txt, tw, twt, g));
   return MOE_OK;
 }
 
@@ -1114,6 +1128,7 @@ moe_status_t moe_linear(int dtype, const void* x, int64_t ldx, const float* x_sc
   g.T = T;
   g.N = N;
   g.nk = static_cast<int>((static_cast<int64_t>(K) * es + moe::kTileKBytes - 1) / moe::kTileKBytes);
+  g.nk_full = K / (moe::kTileKBytes / es);
   g.f16 = dtype == MOE_DT_FP16;
   g.x_scale = x_scale;
   g.w_scale = w_scale;
