@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   const uint32_t tmem_base = *tmem_slot;
 
   if (warp == 0 || warp == 2) {
-    if (lane == 0) {
+    if (elect_one()) {
       const bool is_w = warp == 0;
       const CUtensorMap* tm = is_w ? &tmW : &tmX;
       const CUtensorMap* tail = is_w ? &tmWt : &tmXt;
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kSplitThreads)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc = FP8 ? idesc_e4m3(kTileM, BN) : idesc_16bit(kTileM, BN, g.f16);
       int stage = 0;
       uint32_t phase = 0;
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int b_rows = g.tn / 2;  // weight rows in each CTA
 
   if (warp == 0 || warp == 2) {
-    if (lane == 0) {
+    if (elect_one()) {
       const bool is_x = warp == 0;
       const CUtensorMap* tm = is_x ? &tmX : &tmW;
       const CUtensorMap* tail = is_x ? &tmXt : &tmWt;
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
+    if (rank == 0 && elect_one()) {
       const uint32_t idesc = FP8 ? idesc_e4m3(2 * kTileM, g.tn) : idesc_16bit(2 * kTileM, g.tn, g.f16);
       int stage = 0;
       uint32_t phase = 0;

@@ -98,6 +98,21 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   return mbar_wait_slow(a, parity, abort_flag);
 }
 
+// True in one lane of a converged warp. The compiler knows a region under this
+// predicate to be run by a single thread and keeps tensor-core descriptors and
+// copy operands in uniform registers there; under `lane == 0` it moves them for
+// every instruction (measured for a stage of eight MMAs and a commit, N = 16:
+// 763 clocks under `lane == 0`, 403 under this).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "elect.sync _|P, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, P;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
 // ---------------------------------------------------------------- TMA
 
 __device__ __forceinline__ uint64_t policy_evict_first() {
