@@ -393,39 +393,50 @@ constexpr int kPromoteAtoms = 8;
 constexpr int kPromoteTn = 128;  // outputs per tile with PROMOTE: 64 running sums per epilogue thread
 
 struct TileCfg {
-  static constexpr int kStages = 3;
+  static constexpr int kMaxStages = 5;
   static constexpr int kAtom = kTileM * kTileKBytes;
   static constexpr int kABytes = kAtom * kLinAtoms;  // 128 tokens
-  static constexpr int kStageBytes = 2 * kABytes;    // then up to 128 weight rows
-  static constexpr int kStageOut = kStages * kStageBytes;
-  static constexpr int kWarpOut = 2048;  // 32 rows x 64 bytes
-  static constexpr int kVecOffset = kStageOut + kTileEpiWarps * kWarpOut;  // per warp: [scale, bias][4][32]
-  static constexpr int kBarOffset = kVecOffset + kTileEpiWarps * 2 * 4 * 32 * 4;
-  static constexpr int kBytes = kBarOffset + (2 * kStages + 5) * 8 + 16 + 1024;  // + alignment slack
+  static constexpr int kWarpOut = 2048;              // 32 rows x 64 bytes
+  static constexpr int kBarOffset = kTileEpiWarps * kWarpOut;
+  static constexpr int kStageOffset = kBarOffset + 1024;
   static constexpr int kTmemCols = 512;
-  static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
+  static_assert((2 * kMaxStages + 5) * 8 + 8 <= 1024, "barriers");
+  // a stage: 128 tokens, then tn / 2 weight rows, of kLinAtoms atoms
+  __host__ __device__ static constexpr int stage_bytes(int tn) { return kABytes + tn / 2 * kTileKBytes * kLinAtoms; }
+  __host__ __device__ static constexpr int stages(int tn) {
+    const int fit = (227 * 1024 - 1024 - kStageOffset) / stage_bytes(tn);  // less the alignment slack
+    return fit < kMaxStages ? fit : kMaxStages;
+  }
+  __host__ __device__ static constexpr int bytes(int tn) { return kStageOffset + stages(tn) * stage_bytes(tn) + 1024; }
 };
 
 // Byte offset of 16-byte unit u of row r in a warp's 32 x 64-byte staging: the
 // XOR spreads both the row-wise and the row-group-wise accesses over all banks.
 __device__ __forceinline__ int stage_off(int r, int u) { return r * 64 + ((u ^ ((r >> 1) & 3)) << 4); }
 
-// Rows row0.. of a [T, N] matrix, 64 bytes each from column n0 (`cols` valid),
-// to a warp's staging. `vec`: 16-byte accesses are aligned and every column is valid.
+// 64 bytes of each of the rows row0.. of a [T, N] matrix from column n0, as the
+// warp's lanes hold them: 8 rows x 4 units per register.
 template <typename TE>
-__device__ __forceinline__ void stage_load(uint8_t* st, const TE* src, size_t ld, int row0, int T, int n0, int cols,
-                                           bool vec, int lane) {
-  if (vec) {
-    uint4 v[4];
+__device__ __forceinline__ void fetch_rows(uint4 (&v)[4], const TE* src, size_t ld, int row0, int T, int n0, int lane) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 8 + (lane >> 2);
-      v[i] = row0 + r < T ? *reinterpret_cast<const uint4*>(src + (row0 + r) * ld + n0 + (lane & 3) * (16 / sizeof(TE)))
-                          : make_uint4(0, 0, 0, 0);
-    }
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2);
+    v[i] = row0 + r < T ? *reinterpret_cast<const uint4*>(src + (row0 + r) * ld + n0 + (lane & 3) * (16 / sizeof(TE)))
+                        : make_uint4(0, 0, 0, 0);
+  }
+}
+
+__device__ __forceinline__ void stage_put(uint8_t* st, const uint4 (&v)[4], int lane) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(st + stage_off(i * 8 + (lane >> 2), lane & 3)) = v[i];
-  } else if (lane < cols) {
+  for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(st + stage_off(i * 8 + (lane >> 2), lane & 3)) = v[i];
+}
+
+// The same rows into the staging value by value: unaligned rows, or `cols`
+// columns at the end of the matrix.
+template <typename TE>
+__device__ __forceinline__ void stage_load_cols(uint8_t* st, const TE* src, size_t ld, int row0, int T, int n0,
+                                                int cols, int lane) {
+  if (lane < cols) {
     const int b = lane * static_cast<int>(sizeof(TE));
 #pragma unroll 8
     for (int r = 0; r < 32; ++r)
@@ -452,27 +463,21 @@ __device__ __forceinline__ void stage_store(const uint8_t* st, TE* dst, size_t l
   }
 }
 
-template <typename TX>
-__device__ __forceinline__ void unpack_unit(const uint4& v, float* f) {
-  unpack2(v.x, TX(), f[0], f[1]);
-  unpack2(v.y, TX(), f[2], f[3]);
-  unpack2(v.z, TX(), f[4], f[5]);
-  unpack2(v.w, TX(), f[6], f[7]);
-}
-
 // Residual, rounding and store of 32 columns n0.. of this warp's 32 rows
-// (16-bit results): thread = row, through the staging.
+// (16-bit results): thread = row, through the staging. `res`: the residual
+// fetched ahead (fetch_rows), where whole 16-byte units could be.
 template <typename TX>
-__device__ __forceinline__ void tile_store_16(const LinearArgs& g, uint8_t* st, float (&v)[32], int row0, int n0,
-                                              int lane) {
+__device__ __forceinline__ void tile_store_16(const LinearArgs& g, uint8_t* st, float (&v)[32], const uint4 (&res)[4],
+                                              int row0, int n0, int lane) {
   const int cols = min(32, g.N - n0);
   if (g.residual) {
-    stage_load(st, static_cast<const TX*>(g.residual), g.ldr, row0, g.T, n0, cols, g.res_vec && cols == 32, lane);
+    if (g.res_vec && cols == 32) stage_put(st, res, lane);
+    else stage_load_cols(st, static_cast<const TX*>(g.residual), g.ldr, row0, g.T, n0, cols, lane);
     __syncwarp();
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       float f[8];
-      unpack_unit<TX>(*reinterpret_cast<const uint4*>(st + stage_off(lane, u)), f);
+      unpack8<TX>(*reinterpret_cast<const uint4*>(st + stage_off(lane, u)), f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[8 * u + i] += f[i];
     }
@@ -496,7 +501,14 @@ __device__ __forceinline__ void tile_store_32(const LinearArgs& g, uint8_t* st, 
     const int cols = min(16, g.N - c0);
     if (cols <= 0) return;
     if (g.residual) {
-      stage_load(st, static_cast<const float*>(g.residual), g.ldr, row0, g.T, c0, cols, g.res_vec && cols == 16, lane);
+      const float* src = static_cast<const float*>(g.residual);
+      if (g.res_vec && cols == 16) {
+        uint4 res[4];
+        fetch_rows(res, src, g.ldr, row0, g.T, c0, lane);
+        stage_put(st, res, lane);
+      } else {
+        stage_load_cols(st, src, g.ldr, row0, g.T, c0, cols, lane);
+      }
       __syncwarp();
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -539,8 +551,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOffset);
-  uint64_t* empty = full + L::kStages;
-  uint64_t* acc_full = empty + L::kStages;
+  uint64_t* empty = full + L::kMaxStages;
+  uint64_t* acc_full = empty + L::kMaxStages;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -549,8 +561,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
+  const int n_stages = L::stages(g.tn);
+  const int stage_bytes = L::stage_bytes(g.tn);
+  uint8_t* stages = smem + L::kStageOffset;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < L::kStages; ++s) {
+    for (int s = 0; s < n_stages; ++s) {
       mbar_init(&full[s], 2);  // armed by rank 0's two producers with both CTAs' bytes
       mbar_init(&empty[s], 1);
     }
@@ -603,11 +618,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (!ok) break;
           const int na = min(kLinAtoms, g.nk - ks * kLinAtoms);
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(2 * na * atom_bytes));
-          load_stage<KE, true>(smem + stage * L::kStageBytes + off, tm, tail, nullptr,
+          load_stage<KE, true>(stages + stage * stage_bytes + off, tm, tail, nullptr,
                                full0 + 8u * static_cast<uint32_t>(stage), ks, row0, atom_bytes, g, pol);
           pending |= 1u << stage;
           parity = (parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == L::kStages) {
+          if (++stage == n_stages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -615,7 +630,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       if (!ok) {
         if (rank == 0) {
-          for (int s = 0; s < L::kStages; ++s)
+          for (int s = 0; s < n_stages; ++s)
             if ((pending >> s) & 1u) drain_wait(&full[s], (parity >> s) & 1u);
         } else if (pending) {
           // rank 1's copies complete on rank 0's barriers, which it cannot wait
@@ -646,7 +661,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const int na = min(kLinAtoms, g.nk - ks * kLinAtoms);
-            const uint32_t a_addr = smem_u32(smem + stage * L::kStageBytes);
+            const uint32_t a_addr = smem_u32(stages + stage * stage_bytes);
 #pragma unroll
             for (int a = 0; a < kLinAtoms; ++a) {
               if (a < na) {
@@ -661,7 +676,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               }
             }
             umma_commit_pair_multicast(&empty[stage], 3);
-            if (++stage == L::kStages) {
+            if (++stage == n_stages) {
               stage = 0;
               phase ^= 1u;
             }
@@ -679,9 +694,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int ew = warp - 4;
     const int q = ew & 3;     // TMEM lane quarter
     const int half = ew >> 2;  // columns 32 c.. with c % 2 == half
-    uint8_t* st = smem + L::kStageOut + ew * L::kWarpOut;
-    float* ws_sm = reinterpret_cast<float*>(smem + L::kVecOffset) + ew * 256;  // this warp's columns, by chunk
-    float* b_sm = ws_sm + 128;
+    uint8_t* st = smem + ew * L::kWarpOut;
     const uint32_t acc_empty0 = mapa_shared(smem_u32(acc_empty), 0);
     const int chunks = g.tn / 32;
     int j = 0;
@@ -691,41 +704,56 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tile_coords(g, tile, mt, nt);
       const int row0 = mt * 2 * kTileM + static_cast<int>(rank) * kTileM + 32 * q;
       const int t = row0 + lane;
-      // weight scales and bias of this warp's columns, fetched while the sum is being built
-      for (int c = half; c < chunks; c += 2) {
-        const int n = nt * g.tn + 32 * c + lane;
-        ws_sm[16 * (c - half) + lane] = FP8 && n < g.N ? __ldg(g.w_scale + static_cast<size_t>(n) * g.w_scale_step) : 1.f;
-        b_sm[16 * (c - half) + lane] = g.bias && n < g.N ? load_typed(g.bias, g.bias_dt, n) : 0.f;
-      }
       const float xs = g.x_scale && t < g.T ? __ldg(g.x_scale + t) : 1.f;
-      __syncwarp();
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
 
+      // weight scale, bias and residual of chunk c, fetched a chunk ahead
+      float ws = 1.f, bias = 0.f;
+      uint4 res[4];
+      auto fetch = [&](int c) {
+        const int n0 = nt * g.tn + 32 * c;
+        const bool in = c < chunks && row0 < g.T && n0 + lane < g.N;
+        if (FP8) ws = in ? __ldg(g.w_scale + static_cast<size_t>(n0 + lane) * g.w_scale_step) : 1.f;
+        if (g.bias) bias = in ? load_typed(g.bias, g.bias_dt, n0 + lane) : 0.f;
+        if (!PROMOTE && g.res_vec && c < chunks && row0 < g.T && n0 + 32 <= g.N)
+          fetch_rows(res, static_cast<const unsigned short*>(g.residual), g.ldr, row0, g.T, n0, lane);
+      };
       auto finish = [&](float (&v)[32], int c) {
         const int n0 = nt * g.tn + 32 * c;
-        if (row0 >= g.T || n0 >= g.N) return;
-        const float4* ws4 = reinterpret_cast<const float4*>(ws_sm + 16 * (c - half));
-        const float4* b4 = reinterpret_cast<const float4*>(b_sm + 16 * (c - half));
+        const bool in = row0 < g.T && n0 < g.N;
+        float* vec = reinterpret_cast<float*>(st);  // scales and bias to every lane, through the staging
+        if (FP8) vec[lane] = ws;
+        vec[32 + lane] = bias;
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if (FP8) {
-            const float4 w = ws4[i];
+            const float4 w = reinterpret_cast<const float4*>(vec)[i];
             v[4 * i] *= xs * w.x;
             v[4 * i + 1] *= xs * w.y;
             v[4 * i + 2] *= xs * w.z;
             v[4 * i + 3] *= xs * w.w;
           }
-          const float4 b = b4[i];
+          const float4 b = reinterpret_cast<const float4*>(vec)[8 + i];
           v[4 * i] += b.x;
           v[4 * i + 1] += b.y;
           v[4 * i + 2] += b.z;
           v[4 * i + 3] += b.w;
         }
+        __syncwarp();
+        if (!in) return;
+        uint4 r[4];
+        if (!PROMOTE) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) r[i] = res[i];
+        }
+        fetch(c + 2);
         apply_act(v, g.act);
         if (PROMOTE) tile_store_32(g, st, v, row0, n0, lane);
-        else if (g.out_dt == 0) tile_store_16<__nv_bfloat16>(g, st, v, row0, n0, lane);
-        else tile_store_16<__half>(g, st, v, row0, n0, lane);
+        else if (g.out_dt == 0) tile_store_16<__nv_bfloat16>(g, st, v, r, row0, n0, lane);
+        else tile_store_16<__half>(g, st, v, r, row0, n0, lane);
       };
+      fetch(half);
       auto release = [&](int acc) {
         tc_fence_before();
         __syncwarp();
@@ -771,10 +799,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (c + 2 >= chunks) release(acc);
           finish(v, c);
         }
-        if (half >= chunks) release(acc);  // one-chunk tiles: the second half of the warps reads nothing
         ++j;
       }
-      __syncwarp();  // the scales and bias are rewritten next
     }
   }
 

@@ -489,7 +489,7 @@ moe_status_t launch_linear_tile(const LinearCall& c, int tn, cudaStream_t s) {
   if (r != MOE_OK) return r;
   auto kern = moe::k_linear_tile<FP8, PROMOTE>;
   static std::atomic<int> attr_set[64];
-  r = set_smem_attr(kern, L::kBytes, attr_set);
+  r = set_smem_attr(kern, 227 * 1024, attr_set);
   if (r != MOE_OK) return r;
   moe::LinearArgs g = c.g;
   g.tn = tn;
@@ -509,7 +509,7 @@ moe_status_t launch_linear_tile(const LinearCall& c, int tn, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
   cfg.blockDim = dim3(moe::kTileThreads);
-  cfg.dynamicSmemBytes = L::kBytes;
+  cfg.dynamicSmemBytes = L::bytes(tn);
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;

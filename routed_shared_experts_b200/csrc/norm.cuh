@@ -35,13 +35,17 @@ struct NormArgs {
   uint8_t* sbytes;     // [T, H / 32] (kNormMx)
 };
 
+// Two rounded values in a word, low half first: the packing conversion (the
+// conversions of single values run at an eighth of its rate).
 __device__ __forceinline__ uint32_t pack2(float lo, float hi, __nv_bfloat16) {
-  return static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(lo))) |
-         (static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(hi))) << 16);
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi, __half) {
-  return static_cast<uint32_t>(__half_as_ushort(__float2half_rn(lo))) |
-         (static_cast<uint32_t>(__half_as_ushort(__float2half_rn(hi))) << 16);
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 template <typename TX>
