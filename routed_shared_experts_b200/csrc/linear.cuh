@@ -19,8 +19,9 @@
 // tokens on N, and the K axis split over the S CTAs of a cluster. Each CTA
 // leaves its fp32 partial tile in its own shared memory; after a cluster
 // barrier every CTA adds the S partials of its share of the token columns over
-// distributed shared memory, in rank order, and finishes them. No workspace,
-// no atomics: the result does not depend on the order in which CTAs finish.
+// distributed shared memory, its own first and the others in a fixed order, and
+// finishes them. No workspace, no atomics: the result does not depend on the
+// order in which CTAs finish.
 // What bounds it: with few tokens the weights' stream from HBM, N * K * size
 // bytes, which needs all SMs pulling at once; the K split is what supplies them
 // when N / 128 tiles are fewer than the SMs.
@@ -53,6 +54,7 @@ struct LinearArgs {
   int out_dt;  // MOE_DT_BF16, MOE_DT_FP16 or MOE_DT_F32
   int n_tb;    // token blocks (k_linear_split) or 256-token tiles (k_linear_tile)
   int tn, n_nt;  // k_linear_tile: outputs per tile (a multiple of 32, at most 256), tiles along N
+  int split;     // k_linear_tile with SPLIT: pairs along K
   int out_vec, res_vec;  // k_linear_tile: rows allow 16-byte accesses
 };
 
@@ -75,9 +77,10 @@ __device__ __forceinline__ void apply_act(float (&v)[C], int act) {
 #pragma unroll
       for (int i = 0; i < C; ++i) v[i] = __fdividef(v[i], 1.0f + __expf(-v[i]));
       break;
-    case kActGelu:  // v * Phi(v), by the complementary error function: no cancellation in the left tail
+    case kActGelu:  // v * Phi(v). erff against erfcf(-x): 23 against 31 us at 777 x 2815 x 4096, for an
+                    // absolute error of 2^-24 |v| in the left tail, where the result itself vanishes
 #pragma unroll
-      for (int i = 0; i < C; ++i) v[i] = 0.5f * v[i] * erfcf(-0.70710678118654752f * v[i]);
+      for (int i = 0; i < C; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(0.70710678118654752f * v[i]));
       break;
     case kActGeluTanh:  // 0.5 v (1 + tanh u) = v / (1 + exp(-2u))
 #pragma unroll
@@ -149,28 +152,31 @@ struct SplitCfg {
   static constexpr int kAtomW = kTileM * kTileKBytes;
   static constexpr int kAtomX = BN * kTileKBytes;
   static constexpr int kStageBytes = (kAtomW + kAtomX) * kLinAtoms;
-  // about 100 KB of operands in flight per CTA up to 64 tokens (two CTAs per
-  // SM), all of shared memory above
-  static constexpr int kStages = BN == 16 ? 3 : BN == 32 ? 2 : BN == 64 ? 2 : BN == 128 ? 3 : 2;
-  static constexpr int kBarOffset = kStages * kStageBytes;
-  static constexpr int kBytes = kBarOffset + (2 * kStages + 2) * 8 + 16 + 1024;  // + alignment slack
+  static constexpr int kMaxStages = 6;
+  static constexpr int kStageOffset = 1024;  // after the barriers
   static constexpr int kTmemCols = BN < 32 ? 32 : BN;
   static_assert(kStageBytes % 1024 == 0, "stages start on 1024-byte swizzle boundaries");
-  static_assert(BN * kTileM * 4 <= kBarOffset, "the partial tile fits the stages it replaces");
+  static_assert((2 * kMaxStages + 2) * 8 + 8 <= kStageOffset, "barriers");
+  // as many stages as fit `bytes` of shared memory (one CTA per SM, or two)
+  __host__ __device__ static constexpr int stages(int bytes) {
+    const int fit = (bytes - 1024 - kStageOffset) / kStageBytes;  // less the alignment slack
+    return fit < kMaxStages ? fit : kMaxStages;
+  }
+  __host__ __device__ static constexpr int bytes(int n_stages) { return kStageOffset + n_stages * kStageBytes + 1024; }
+  static_assert(BN * kTileM * 4 <= 2 * kStageBytes, "the partial tile fits the stages it replaces");
 };
 
 // Scale, bias, activation, residual and store of C tokens t0.. of output n.
 template <int C>
-__device__ __forceinline__ void split_finish(const LinearArgs& g, float (&v)[C], int n, int t0, int t_end, float ws,
-                                             float bias) {
-  float r[C];
+__device__ __forceinline__ void split_residual(const LinearArgs& g, float (&r)[C], int n, int t0, int t_end) {
 #pragma unroll
-  for (int i = 0; i < C; ++i) r[i] = 0.f;
-  if (g.residual) {
-#pragma unroll
-    for (int i = 0; i < C; ++i)
-      if (t0 + i < t_end) r[i] = load_residual(g.residual, g.out_dt, (t0 + i) * g.ldr + n);
-  }
+  for (int i = 0; i < C; ++i)
+    r[i] = g.residual && n < g.N && t0 + i < t_end ? load_residual(g.residual, g.out_dt, (t0 + i) * g.ldr + n) : 0.f;
+}
+template <int C>
+__device__ __forceinline__ void split_finish(const LinearArgs& g, float (&v)[C], const float (&r)[C], int n, int t0,
+                                             int t_end, float ws, float bias) {
+  if (n >= g.N) return;
   if (g.x_scale) {
 #pragma unroll
     for (int i = 0; i < C; ++i)
@@ -188,14 +194,15 @@ template <int BN, bool FP8>
 __global__ void __launch_bounds__(kSplitThreads)
     k_linear_split(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWt,
                    const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXt,
-                   const LinearArgs g, int S) {
+                   const LinearArgs g, int S, int n_stages) {
   using L = SplitCfg<BN>;
   constexpr int KE = FP8 ? 128 : 64;  // K elements per atom
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarOffset);
-  uint64_t* empty = full + L::kStages;
-  uint64_t* done = empty + L::kStages;
+  uint8_t* stages = smem + L::kStageOffset;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem);
+  uint64_t* empty = full + L::kMaxStages;
+  uint64_t* done = empty + L::kMaxStages;
   uint64_t* drain = done + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -211,7 +218,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   const int s1 = static_cast<int>(static_cast<long long>(ns) * (rank + 1) / S);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < L::kStages; ++s) {
+    for (int s = 0; s < n_stages; ++s) {
       mbar_init(&full[s], 2);  // each producer arms it with its own bytes
       mbar_init(&empty[s], 1);
     }
@@ -248,17 +255,17 @@ __global__ void __launch_bounds__(kSplitThreads)
         if (!ok) break;
         const int na = min(kLinAtoms, g.nk - ks * kLinAtoms);
         mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(na * atom_bytes));
-        load_stage<KE, false>(smem + stage * L::kStageBytes + off, tm, tail, &full[stage], 0, ks, row0, atom_bytes, g,
+        load_stage<KE, false>(stages + stage * L::kStageBytes + off, tm, tail, &full[stage], 0, ks, row0, atom_bytes, g,
                               pol);
         pending |= 1u << stage;
         parity = (parity & ~(1u << stage)) | (phase << stage);
-        if (++stage == L::kStages) {
+        if (++stage == n_stages) {
           stage = 0;
           phase ^= 1u;
         }
       }
       if (!ok) {
-        for (int s = 0; s < L::kStages; ++s)
+        for (int s = 0; s < n_stages; ++s)
           if ((pending >> s) & 1u) drain_wait(&full[s], (parity >> s) & 1u);
       }
     }
@@ -274,7 +281,7 @@ __global__ void __launch_bounds__(kSplitThreads)
         if (!ok) break;
         tc_fence_after();
         const int na = min(kLinAtoms, g.nk - ks * kLinAtoms);
-        const uint32_t a_addr = smem_u32(smem + stage * L::kStageBytes);
+        const uint32_t a_addr = smem_u32(stages + stage * L::kStageBytes);
 #pragma unroll
         for (int a = 0; a < kLinAtoms; ++a) {
           if (a < na) {
@@ -289,7 +296,7 @@ __global__ void __launch_bounds__(kSplitThreads)
           }
         }
         umma_commit(&empty[stage]);
-        if (++stage == L::kStages) {
+        if (++stage == n_stages) {
           stage = 0;
           phase ^= 1u;
         }
@@ -308,31 +315,43 @@ __global__ void __launch_bounds__(kSplitThreads)
   const int rowi = 32 * q + lane;
   const int n = nt * kTileM + rowi;
   const int nv = min(BN, g.T - t_base);  // tokens of this block
-  float ws = 0.f, bias = 0.f;
+  constexpr int C = 8;  // token columns a thread finishes at a time
+  // S > 1: this CTA finishes columns c_lo .. c_hi - 1
+  const int c_lo = nv * rank / S, c_hi = nv * (rank + 1) / S;
+  float ws = 0.f, bias = 0.f, res[C];
   bool ok = false;
   if (warp >= 3) {
     if (n < g.N) {  // fetched while the sum is still being built
       if (g.x_scale) ws = __ldg(g.w_scale + static_cast<size_t>(n) * g.w_scale_step);
       if (g.bias) bias = load_typed(g.bias, g.bias_dt, n);
     }
+    split_residual(g, res, n, t_base + c_lo, t_base + c_hi);
     ok = mbar_wait(done, 0, abort_flag);
-    __syncwarp();
+    ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
   }
   const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
   if (S == 1) {
-    if (warp >= 3 && __all_sync(0xffffffffu, ok)) {
+    if (ok) {
       for (int c0 = 0; c0 < nv; c0 += 16) {
         float v[16];
         tmem_ld16(t_row + static_cast<uint32_t>(c0), v);
         tmem_wait_ld();
-        if (n < g.N) split_finish<16>(g, v, n, t_base + c0, t_base + nv, ws, bias);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float u[C];
+#pragma unroll
+          for (int i = 0; i < C; ++i) u[i] = v[C * h + i];
+          const int t0 = t_base + c0 + C * h;
+          if (c0 + h > 0) split_residual(g, res, n, t0, t_base + nv);
+          split_finish(g, u, res, n, t0, t_base + nv, ws, bias);
+        }
       }
     }
   } else {
     // the stages are free: every copy has landed and every MMA has read them
-    float* part = reinterpret_cast<float*>(smem);  // [token column][128 outputs]
-    if (warp >= 3 && __all_sync(0xffffffffu, ok)) {
+    float* part = reinterpret_cast<float*>(stages);  // [token column][128 outputs]
+    if (ok) {
       for (int c0 = 0; c0 < nv; c0 += 16) {
         float v[16];
         tmem_ld16(t_row + static_cast<uint32_t>(c0), v);
@@ -343,20 +362,20 @@ __global__ void __launch_bounds__(kSplitThreads)
     }
     cluster_sync_all();
     if (warp >= 3) {
-      constexpr int C = 4;
-      const int c_lo = nv * rank / S, c_hi = nv * (rank + 1) / S;
       const uint32_t part0 = smem_u32(part) + 4u * static_cast<uint32_t>(rowi);
       for (int c0 = c_lo; c0 < c_hi; c0 += C) {
+        if (c0 > c_lo) split_residual(g, res, n, t_base + c0, t_base + c_hi);
         float v[C];
 #pragma unroll
         for (int i = 0; i < C; ++i) v[i] = 0.f;
-        for (int p = 0; p < S; ++p) {
-          const uint32_t peer = mapa_shared(part0, static_cast<uint32_t>(p));
+#pragma unroll 2
+        for (int p = 0; p < S; ++p) {  // from this CTA's own partial tile on, so that the peers' reads spread
+          const uint32_t peer = mapa_shared(part0, static_cast<uint32_t>((rank + p) & (S - 1)));
 #pragma unroll
           for (int i = 0; i < C; ++i)
             if (c0 + i < c_hi) v[i] += ld_shared_cluster_f32(peer + static_cast<uint32_t>((c0 + i) * kTileM * 4));
         }
-        if (n < g.N) split_finish<C>(g, v, n, t_base + c0, t_base + c_hi, ws, bias);
+        split_finish(g, v, res, n, t_base + c0, t_base + c_hi, ws, bias);
       }
     }
     cluster_sync_relaxed();  // no CTA leaves while a peer may still read its partial tile
@@ -381,11 +400,19 @@ __global__ void __launch_bounds__(kSplitThreads)
 // reads and result writes are whole 64-byte row segments and no barrier between
 // warps is needed.
 //
+// SPLIT: the K axis of a tile is divided over the `split` pairs of one cluster,
+// for shapes whose tiles are fewer than the pairs of SMs. As in k_linear_split
+// each CTA leaves its fp32 partial tile in its own shared memory and the CTAs of
+// the same token half finish 128 / split rows each, adding the partials over
+// distributed shared memory in a fixed order.
+//
 // PROMOTE (fp32 results): the tensor core's accumulation is cut every
 // kPromoteAtoms K atoms and the pieces are added in registers in fp32 (round
 // to nearest), which the accumulator's own additions are not: the error of a
 // sum over K = 7168 drops from about 7e-6 to below 1e-6 of its rms. A 16-bit
-// result's rounding hides that error, so those keep one accumulation.
+// result's rounding hides that error, so those keep one accumulation. With
+// SPLIT the pieces are the two halves of a pair's share of K, one in each
+// accumulator.
 
 constexpr int kTileEpiWarps = 8;
 constexpr int kTileThreads = 128 + 32 * kTileEpiWarps;
@@ -541,7 +568,116 @@ __device__ __forceinline__ void tile_coords(const LinearArgs& g, int tile, int& 
   mt = band * kBand + (i - nt * rows);
 }
 
-template <bool FP8, bool PROMOTE>
+// SPLIT: rows [lo, hi) of this CTA's 128 from the S partial tiles, one warp per
+// row, four columns per lane. A partial tile is [128][tn] fp32 in 16-byte units,
+// unit u of row r at u ^ (r & 7).
+__device__ __forceinline__ int part_unit(int r, int u, int tn) { return r * (tn / 4) + (u ^ (r & 7)); }
+
+__device__ __forceinline__ float4 ld_shared_cluster_f32x4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+
+// Four consecutive values (`cols` of them valid) of the residual and the result.
+__device__ __forceinline__ void load_res4(const LinearArgs& g, size_t at, int cols, float (&res)[4]) {
+  if (g.res_vec && cols == 4) {
+    if (g.out_dt == 4) {
+      const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(g.residual) + at);
+      res[0] = f.x, res[1] = f.y, res[2] = f.z, res[3] = f.w;
+    } else {
+      const uint2 f = *reinterpret_cast<const uint2*>(static_cast<const unsigned short*>(g.residual) + at);
+      if (g.out_dt == 0) {
+        unpack2(f.x, __nv_bfloat16(), res[0], res[1]);
+        unpack2(f.y, __nv_bfloat16(), res[2], res[3]);
+      } else {
+        unpack2(f.x, __half(), res[0], res[1]);
+        unpack2(f.y, __half(), res[2], res[3]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < cols) res[i] = load_residual(g.residual, g.out_dt, at + i);
+  }
+}
+
+__device__ __forceinline__ void store4(const LinearArgs& g, size_t at, int cols, const float (&v)[4]) {
+  if (g.out_vec && cols == 4) {
+    if (g.out_dt == 4)
+      *reinterpret_cast<float4*>(static_cast<float*>(g.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    else if (g.out_dt == 0)
+      *reinterpret_cast<uint2*>(static_cast<unsigned short*>(g.out) + at) =
+          make_uint2(pack2(v[0], v[1], __nv_bfloat16()), pack2(v[2], v[3], __nv_bfloat16()));
+    else
+      *reinterpret_cast<uint2*>(static_cast<unsigned short*>(g.out) + at) =
+          make_uint2(pack2(v[0], v[1], __half()), pack2(v[2], v[3], __half()));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < cols) store_typed(g.out, g.out_dt, at + i, v[i]);
+  }
+}
+
+__device__ __forceinline__ void split_rows(const LinearArgs& g, uint32_t part, uint32_t ctarank, int mt, int nt, int ew,
+                                           int lane) {
+  const int S = g.split;
+  const int lo = kTileM / S * static_cast<int>(ctarank >> 1), hi = lo + kTileM / S;
+  const int t0 = mt * 2 * kTileM + static_cast<int>(ctarank & 1u) * kTileM;
+  for (int u = lane; u < g.tn / 4; u += 32) {
+    const int n = nt * g.tn + 4 * u;
+    const int cols = min(4, g.N - n);
+    if (cols <= 0) continue;
+    float ws[4], bias[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ws[i] = g.w_scale && i < cols ? __ldg(g.w_scale + static_cast<size_t>(n + i) * g.w_scale_step) : 1.f;
+      bias[i] = g.bias && i < cols ? load_typed(g.bias, g.bias_dt, n + i) : 0.f;
+    }
+    // two rows at a time: their remote loads are in flight together
+    constexpr int R = 2;
+    for (int r0 = lo + R * ew; r0 < hi && t0 + r0 < g.T; r0 += R * kTileEpiWarps) {
+      float res[R][4], v[R][4], xs[R];
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const int t = t0 + r0 + j;
+        const bool in = t < g.T;
+        xs[j] = g.x_scale && in ? __ldg(g.x_scale + t) : 1.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] = res[j][i] = 0.f;
+        if (g.residual && in) load_res4(g, t * g.ldr + n, cols, res[j]);
+      }
+#pragma unroll 2
+      for (int p = 0; p < S; ++p) {  // from this CTA's own partial tile on, so that the peers' reads spread
+        const uint32_t peer = mapa_shared(part, (ctarank + 2u * static_cast<uint32_t>(p)) & (2u * S - 1u));
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          const float4 f = ld_shared_cluster_f32x4(peer + 16u * static_cast<uint32_t>(part_unit(r0 + j, u, g.tn)));
+          v[j][0] += f.x;
+          v[j][1] += f.y;
+          v[j][2] += f.z;
+          v[j][3] += f.w;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const int t = t0 + r0 + j;
+        if (t >= g.T) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] = v[j][i] * (xs[j] * ws[i]) + bias[i];
+        apply_act(v[j], g.act);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] += res[j][i];
+        store4(g, t * g.ldo + n, cols, v[j]);
+      }
+    }
+  }
+}
+
+template <bool FP8, bool PROMOTE, bool SPLIT>
 __global__ void __launch_bounds__(kTileThreads, 1)
     k_linear_tile(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXt,
                   const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWt,
@@ -560,7 +696,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t ctarank = cluster_ctarank();
+  const uint32_t rank = ctarank & 1u;      // in the pair
+  const uint32_t leader = ctarank & ~1u;   // the pair's rank 0
   const int n_stages = L::stages(g.tn);
   const int stage_bytes = L::stage_bytes(g.tn);
   uint8_t* stages = smem + L::kStageOffset;
@@ -588,11 +726,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
 
   const int total = g.n_tb * g.n_nt;
-  const int unit0 = static_cast<int>(blockIdx.x >> 1);
-  const int n_units = static_cast<int>(gridDim.x >> 1);
-  const int ns = (g.nk + kLinAtoms - 1) / kLinAtoms;  // stages per tile
-  const int kc_stages = PROMOTE ? kPromoteAtoms / kLinAtoms : ns;
-  const int n_kc = PROMOTE ? (ns + kc_stages - 1) / kc_stages : 1;  // accumulations per tile
+  // SPLIT: one tile per cluster; else the pairs stride over the tiles
+  const int unit0 = static_cast<int>(SPLIT ? blockIdx.x / (2u * static_cast<unsigned>(g.split)) : blockIdx.x >> 1);
+  const int n_units = SPLIT ? total : static_cast<int>(gridDim.x >> 1);
+  // stages of a tile along K (SPLIT: this pair's share), and accumulations they are cut into
+  const int ns_all = (g.nk + kLinAtoms - 1) / kLinAtoms;
+  const int s_first = SPLIT ? static_cast<int>(static_cast<long long>(ns_all) * (ctarank >> 1) / g.split) : 0;
+  const int s_end = SPLIT ? static_cast<int>(static_cast<long long>(ns_all) * ((ctarank >> 1) + 1) / g.split) : ns_all;
+  const int ns = s_end - s_first;
+  const int kc_stages = !PROMOTE ? ns : SPLIT ? (ns + 1) / 2 : kPromoteAtoms / kLinAtoms;
+  const int n_kc = PROMOTE ? (ns + kc_stages - 1) / kc_stages : 1;
   const int b_rows = g.tn / 2;  // weight rows in each CTA
 
   if (warp == 0 || warp == 2) {
@@ -601,7 +744,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const CUtensorMap* tm = is_x ? &tmX : &tmW;
       const CUtensorMap* tail = is_x ? &tmXt : &tmWt;
       const uint64_t pol = policy_evict_last();  // both operands are read by several tiles
-      const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+      const uint32_t full0 = mapa_shared(smem_u32(full), leader);
       const int atom_bytes = is_x ? L::kAtom : b_rows * kTileKBytes;
       const int off = is_x ? 0 : L::kABytes;
       int stage = 0;
@@ -613,7 +756,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tile_coords(g, tile, mt, nt);
         const int row0 = is_x ? mt * 2 * kTileM + static_cast<int>(rank) * kTileM
                               : nt * g.tn + static_cast<int>(rank) * b_rows;
-        for (int ks = 0; ks < ns; ++ks) {
+        for (int ks = s_first; ks < s_end; ++ks) {
           ok = mbar_wait(&empty[stage], phase ^ 1u, abort_flag);
           if (!ok) break;
           const int na = min(kLinAtoms, g.nk - ks * kLinAtoms);
@@ -648,6 +791,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       uint32_t phase = 0;
       bool ok = true;
       int j = 0;  // accumulation counter: accumulator j % 2
+      const uint16_t pair_mask = static_cast<uint16_t>(3u << leader);
       for (int tile = unit0; tile < total && ok; tile += n_units) {
         for (int kc = 0; kc < n_kc && ok; ++kc, ++j) {
           const int acc = j & 1;
@@ -655,7 +799,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (!ok) break;
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * 256);
-          const int s_lo = kc * kc_stages, s_hi = min(ns, s_lo + kc_stages);
+          const int s_lo = s_first + kc * kc_stages, s_hi = min(s_end, s_lo + kc_stages);
           for (int ks = s_lo; ks < s_hi; ++ks) {
             ok = mbar_wait(&full[stage], phase, abort_flag);
             if (!ok) break;
@@ -675,27 +819,54 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
               }
             }
-            umma_commit_pair_multicast(&empty[stage], 3);
+            umma_commit_pair_multicast(&empty[stage], pair_mask);
             if (++stage == n_stages) {
               stage = 0;
               phase ^= 1u;
             }
           }
-          if (ok) umma_commit_pair_multicast(&acc_full[acc], 3);
+          if (ok) umma_commit_pair_multicast(&acc_full[acc], pair_mask);
         }
       }
       if (!ok) {
-        umma_commit_pair(mapa_shared(smem_u32(drain), 0));
+        umma_commit_pair(mapa_shared(smem_u32(drain), leader));
         drain_wait(drain, 0);
       }
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (SPLIT && warp >= 4) {
+    // partial tile to shared memory: the stages are free once the last accumulation is complete
+    const int q = warp & 3;
+    const int r = 32 * q + lane;
+    bool ok = true;
+    for (int kc = 0; kc < n_kc && ok; ++kc) ok = mbar_wait(&acc_full[kc], 0, abort_flag);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) {
+      tc_fence_after();
+      float4* part = reinterpret_cast<float4*>(stages);
+      for (int c = (warp - 4) >> 2; c < g.tn / 32; c += 2) {
+        const uint32_t at = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(32 * c);
+        float v[32];
+        tmem_ld32(at, v);
+        tmem_wait_ld();
+        if (PROMOTE && n_kc == 2) {
+          float v2[32];
+          tmem_ld32(at + 256, v2);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] += v2[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          part[part_unit(r, 8 * c + i, g.tn)] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      }
+    }
+  } else if (!SPLIT && warp >= 4) {
     const int ew = warp - 4;
     const int q = ew & 3;     // TMEM lane quarter
     const int half = ew >> 2;  // columns 32 c.. with c % 2 == half
     uint8_t* st = smem + ew * L::kWarpOut;
-    const uint32_t acc_empty0 = mapa_shared(smem_u32(acc_empty), 0);
+    const uint32_t acc_empty0 = mapa_shared(smem_u32(acc_empty), leader);
     const int chunks = g.tn / 32;
     int j = 0;
     bool ok = true;
@@ -804,6 +975,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   }
 
+  if constexpr (SPLIT) {
+    cluster_sync_all();  // every partial tile is written
+    if (warp >= 4) {
+      int mt, nt;
+      tile_coords(g, unit0, mt, nt);
+      split_rows(g, smem_u32(stages), ctarank, mt, nt, warp - 4, lane);
+    }
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync_relaxed();  // no CTA leaves while its peer may still signal its barriers

@@ -449,7 +449,6 @@ struct LinearCall {
 template <int BN, bool FP8>
 moe_status_t launch_linear_split(const LinearCall& c, int S, cudaStream_t s) {
   using L = moe::SplitCfg<BN>;
-  static_assert(L::kBytes <= 227 * 1024, "shared memory per CTA");
   CUtensorMap tw, twt, tx, txt;
   moe_status_t r = make_linear_maps(&tw, &twt, c.dtype, c.w, c.g.N, c.K, c.ldw, moe::kTileM);
   if (r != MOE_OK) return r;
@@ -457,12 +456,14 @@ moe_status_t launch_linear_split(const LinearCall& c, int S, cudaStream_t s) {
   if (r != MOE_OK) return r;
   auto kern = moe::k_linear_split<BN, FP8>;
   static std::atomic<int> attr_set[64];
-  r = set_smem_attr(kern, L::kBytes, attr_set);
+  r = set_smem_attr(kern, 227 * 1024, attr_set);
   if (r != MOE_OK) return r;
   moe::LinearArgs g = c.g;
-  g.n_tb = (g.T + BN - 1) / BN;
-  const int64_t ctas = static_cast<int64_t>((g.N + moe::kTileM - 1) / moe::kTileM) * g.n_tb * S;
-  if (ctas > INT32_MAX) return MOE_ERR_SHAPE;
+  g.n_tb = 1;
+  const int ctas = (g.N - 1) / moe::kTileM * S + S;
+  // one CTA per SM takes all of its shared memory for stages; more CTAs than
+  // SMs share it two by two (N = 20000, K = 2048, one token: 16.7 against 21.2 us)
+  const int n_stages = L::stages(ctas <= num_sms() ? 227 * 1024 : 113 * 1024);
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = static_cast<unsigned>(S);
@@ -471,23 +472,23 @@ moe_status_t launch_linear_split(const LinearCall& c, int S, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(moe::kSplitThreads);
-  cfg.dynamicSmemBytes = L::kBytes;
+  cfg.dynamicSmemBytes = L::bytes(n_stages);
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  MOE_CK(cudaLaunchKernelEx(&cfg, kern, tw, twt, tx, txt, g, S));
+  MOE_CK(cudaLaunchKernelEx(&cfg, kern, tw, twt, tx, txt, g, S, n_stages));
   return MOE_OK;
 }
 
-template <bool FP8, bool PROMOTE>
-moe_status_t launch_linear_tile(const LinearCall& c, int tn, cudaStream_t s) {
+template <bool FP8, bool PROMOTE, bool SPLIT>
+moe_status_t launch_linear_tile(const LinearCall& c, int tn, int split, cudaStream_t s) {
   using L = moe::TileCfg;
   CUtensorMap tx, txt, tw, twt;
   moe_status_t r = make_linear_maps(&tx, &txt, c.dtype, c.x, c.g.T, c.K, c.ldx, moe::kTileM);
   if (r != MOE_OK) return r;
   r = make_linear_maps(&tw, &twt, c.dtype, c.w, c.g.N, c.K, c.ldw, tn / 2);
   if (r != MOE_OK) return r;
-  auto kern = moe::k_linear_tile<FP8, PROMOTE>;
+  auto kern = moe::k_linear_tile<FP8, PROMOTE, SPLIT>;
   static std::atomic<int> attr_set[64];
   r = set_smem_attr(kern, 227 * 1024, attr_set);
   if (r != MOE_OK) return r;
@@ -496,18 +497,19 @@ moe_status_t launch_linear_tile(const LinearCall& c, int tn, cudaStream_t s) {
   g.n_tb = (g.T + 2 * moe::kTileM - 1) / (2 * moe::kTileM);
   g.n_nt = (g.N + tn - 1) / tn;
   const int64_t tiles = static_cast<int64_t>(g.n_tb) * g.n_nt;
-  if (tiles > INT32_MAX / 2) return MOE_ERR_SHAPE;
+  if (tiles > INT32_MAX / 16) return MOE_ERR_SHAPE;
+  g.split = split;
   const int os = float_size(g.out_dt);
   g.out_vec = aligned16(g.out) && g.ldo * os % 16 == 0;
   g.res_vec = g.residual && aligned16(g.residual) && g.ldr * os % 16 == 0;
   const int pairs = num_sms() / 2;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.x = static_cast<unsigned>(SPLIT ? 2 * split : 2);
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
+  cfg.gridDim = dim3(static_cast<unsigned>(SPLIT ? 2 * tiles * split : 2 * (tiles < pairs ? tiles : pairs)));
   cfg.blockDim = dim3(moe::kTileThreads);
   cfg.dynamicSmemBytes = L::bytes(tn);
   cfg.stream = s;
@@ -518,30 +520,93 @@ moe_status_t launch_linear_tile(const LinearCall& c, int tn, cudaStream_t s) {
 }
 
 struct LinearPlan {
-  int bn, split;  // k_linear_split: tokens per tile, CTAs along K
-  int tn;         // k_linear_tile: outputs per tile, or 0
+  int bn;     // k_linear_split: tokens per tile
+  int split;  // CTAs (k_linear_split) or pairs (k_linear_tile) along K
+  int tn;     // k_linear_tile: outputs per tile, or 0
 };
 
+template <bool FP8, bool PROMOTE>
+moe_status_t launch_linear_pairs(const LinearCall& c, const LinearPlan& p, cudaStream_t s) {
+  if (p.split > 1) return launch_linear_tile<FP8, PROMOTE, true>(c, p.tn, p.split, s);
+  return launch_linear_tile<FP8, PROMOTE, false>(c, p.tn, 1, s);
+}
+
+// Clusters of the pair kernel (2 * split CTAs, one per SM) that run at one time.
+int resident_clusters(int split) {
+  static std::atomic<int> cache[64][3];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+  std::atomic<int>& slot = cache[dev][split / 2];
+  int n = slot.load();
+  if (n) return n;
+  auto kern = moe::k_linear_tile<false, false, true>;
+  static std::atomic<int> attr_set[64];
+  if (set_smem_attr(kern, 227 * 1024, attr_set) != MOE_OK) return 1;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = static_cast<unsigned>(2 * split);
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * split * num_sms()));
+  cfg.blockDim = dim3(moe::kTileThreads);
+  cfg.dynamicSmemBytes = 200 * 1024;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(kern), &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();  // clear: no K split
+    n = 1;
+  }
+  slot.store(n);
+  return n;
+}
+
+// Which kernel and tiles. The times below are nanoseconds measured on B200;
+// they only rank the choices.
 LinearPlan plan_linear(int T, int N, int nk, bool f32_out) {
   LinearPlan p{};
-  if (T > 256) {
-    const int64_t tb = (T + 255) / 256;
-    const int pairs = num_sms() / 2;
-    int64_t best = INT64_MAX;
-    for (int tn = f32_out ? moe::kPromoteTn : 256; tn >= 64; tn -= 32) {
-      const int64_t waves = (tb * ((N + tn - 1) / tn) + pairs - 1) / pairs;
-      const int64_t cost = waves * (static_cast<int64_t>(nk) * (tn > 128 ? 2 * tn : 200 + tn) + 3000);
-      if (cost < best) {
-        best = cost;
-        p.tn = tn;
-      }
+  const int ns = (nk + moe::kLinAtoms - 1) / moe::kLinAtoms;  // stages along K
+  if (T <= 64) {
+    // Weights on the MMA's M side. The K split that still runs all CTAs at one
+    // time streams the weights fastest (N = K = 2048, one token: 8.6, 7.2, 6.3
+    // us for 1, 2, 4 CTAs per tile and 10.1 for 8, whose clusters no longer
+    // fit; N = K = 7168: 21.7, 19.4, 23.4). fp32 results cut K into pieces of
+    // at most 14 atoms, as far as 8 CTAs go.
+    p.bn = T <= 16 ? 16 : T <= 32 ? 32 : 64;
+    const int tiles = (N - 1) / moe::kTileM + 1;
+    p.split = 1;
+    for (int S = 2; S <= 8 && ns >= S; S *= 2) {
+      const int fit = S == 8 ? num_sms() * 3 / 4 : num_sms();
+      const bool precise = f32_out && (ns + p.split - 1) / p.split > 7;
+      if (static_cast<int64_t>(tiles) * S <= fit || precise) p.split = S;
     }
     return p;
   }
-  p.bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256;
-  const int64_t tiles = static_cast<int64_t>((N + 127) / 128) * ((T + p.bn - 1) / p.bn);
-  p.split = 8;
-  while (p.split > 1 && (tiles * p.split > num_sms() || nk < 4 * p.split)) p.split /= 2;
+  // Tokens on the M side, CTA pairs. ns per K atom and fixed time of a tile by
+  // its width (T = 1024, N = 9 tn, K = 2048 and 8192): the narrow ones are
+  // bound by the copies' round trip over the stages that fit, the widest by
+  // the MMAs (512 clocks an atom at tn = 256).
+  const int64_t tb = (T - 1) / 256 + 1;
+  int64_t best = INT64_MAX;
+  for (int tn = 256; tn >= 64; tn -= 32) {
+    static const int atom_ns[7] = {145, 187, 200, 210, 280, 290, 308};
+    const int64_t a = atom_ns[tn / 32 - 2];
+    const int64_t tiles = tb * ((N - 1) / tn + 1);
+    const int64_t fixed = 4500 + 12 * tn;
+    if (!f32_out || tn <= moe::kPromoteTn) {
+      const int64_t waves = (tiles - 1) / (num_sms() / 2) + 1;
+      const int64_t cost = fixed + waves * nk * a;
+      if (cost < best) best = cost, p.tn = tn, p.split = 1;
+    }
+    // K over 2 or 4 pairs of a cluster: one wave only, and for fp32 results at
+    // most 14 atoms in each of a pair's two accumulations
+    for (int S = 2; S <= 4; S *= 2) {
+      if (ns < 4 * S || (f32_out && (ns + S - 1) / S > 14)) continue;
+      if (tiles > resident_clusters(S)) continue;
+      const int64_t cost = fixed + 3500 + 9 * tn + nk * a / S;  // plus the join
+      if (cost < best) best = cost, p.tn = tn, p.split = S;
+    }
+  }
   return p;
 }
 
@@ -549,20 +614,15 @@ template <bool FP8>
 moe_status_t launch_linear(const LinearCall& c, cudaStream_t s) {
   const bool f32 = c.g.out_dt == MOE_DT_F32;
   const LinearPlan p = plan_linear(c.g.T, c.g.N, c.g.nk, f32);
-  if (p.tn) return f32 ? launch_linear_tile<FP8, true>(c, p.tn, s) : launch_linear_tile<FP8, false>(c, p.tn, s);
-  switch (p.bn) {
-    case 16: return launch_linear_split<16, FP8>(c, p.split, s);
-    case 32: return launch_linear_split<32, FP8>(c, p.split, s);
-    case 64: return launch_linear_split<64, FP8>(c, p.split, s);
-    case 128: return launch_linear_split<128, FP8>(c, p.split, s);
-  }
-  return launch_linear_split<256, FP8>(c, p.split, s);
+  if (p.tn) return f32 ? launch_linear_pairs<FP8, true>(c, p, s) : launch_linear_pairs<FP8, false>(c, p, s);
+  if (p.bn == 16) return launch_linear_split<16, FP8>(c, p.split, s);
+  if (p.bn == 32) return launch_linear_split<32, FP8>(c, p.split, s);
+  return launch_linear_split<64, FP8>(c, p.split, s);
 }
 
 template <int VPL>
 moe_status_t launch_route(const moe::RouteArgs& a, bool softmax, cudaStream_t s) {
-  const moe::RouteGroups G(a.E, a.n_group);
-  const size_t smem = a.n_group > 1 ? moe::kRouteWarps * G.smem_words(a.n_group) * sizeof(float) : 0;
+  const size_t smem = a.n_group > 1 ? moe::kRouteWarps * a.groups.words(a.n_group) * sizeof(float) : 0;
   const int blocks = (a.T + moe::kRouteWarps - 1) / moe::kRouteWarps;
   if (softmax) moe::k_route<VPL, true><<<blocks, moe::kRouteWarps * 32, smem, s>>>(a);
   else moe::k_route<VPL, false><<<blocks, moe::kRouteWarps * 32, smem, s>>>(a);
@@ -1163,7 +1223,7 @@ moe_status_t moe_route(const void* logits, int logits_dtype, int64_t ld, const f
     return MOE_ERR_ALIGNMENT;
   moe::RouteArgs a{logits, static_cast<size_t>(ld), logits_dtype, bias, expert_mask, num_valid, T, E, top_k,
                    n_group, topk_group, group_score == MOE_GROUP_MAX, renormalize, routed_scaling_factor, topk_ids,
-                   topk_weights};
+                   topk_weights, moe::RouteGroups(E, n_group)};
   const bool softmax = score == MOE_SCORE_SOFTMAX;
   cudaStream_t s = as_stream(stream);
   if (E <= 32) return launch_route<1>(a, softmax, s);

@@ -167,13 +167,24 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) k_rmsnorm(const NormArg
     amax = row_reduce<TPR, true>(amax, max_sm);
     const float s = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
     if (row && sub == 0) a.scale[t] = s;
+    // One division per row: dividing every value cost 69 against 50 us at 4096 x
+    // 7168. A subnormal s, whose reciprocal may be infinite, divides.
+    const float inv = __fdiv_rn(1.0f, s);
+    const bool tiny = s < 1.17549435e-38f;
 #pragma unroll
     for (int u = 0; u < V; ++u) {
       const int c = sub + u * TPR;
       if (c < nc) {
+        if (tiny) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[u][i] = __fdiv_rn(z[u][i], s);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[u][i] *= inv;
+        }
         uint32_t q[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = cvt_e4m3x2(__fdiv_rn(z[u][2 * i], s), __fdiv_rn(z[u][2 * i + 1], s));
+        for (int i = 0; i < 4; ++i) q[i] = cvt_e4m3x2(z[u][2 * i], z[u][2 * i + 1]);
         reinterpret_cast<uint2*>(a.codes + base)[c] = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
       }
     }

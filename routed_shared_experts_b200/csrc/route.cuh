@@ -17,16 +17,52 @@
 // gets k distinct experts, so that the slots of the layer's sort and the
 // arrival counts of its stage 2 stay complete whatever the mask leaves.
 //
-// What bounds it: latency, not bytes (a 256-expert fp32 row is 1 KB). The
-// chain is load -> double exp -> (max, sum) -> group choice -> k rounds of
-// arg-max, so the rounds are kept short: c is mapped to an unsigned key with
-// the same order and one round is a redux.max of the key and a redux.min of
-// the index among the lanes that hold it, with each lane's best key kept
-// between rounds.
+// What bounds it: latency and instruction issue, not bytes (a 256-expert fp32
+// row is 1 KB). The chain is load -> double exp -> (max, sum) -> group choice ->
+// k rounds of arg-max. The rounds are kept short: c is mapped to an unsigned key
+// with the same order and one round is a redux.max of the key and a redux.min
+// of the index among the lanes that hold it, with each lane's best key kept
+// between rounds. The exponential is the library's; its sum and quotient use a
+// reciprocal by Newton's iteration, which needs no special cases for a divisor
+// in [1, 512]. The scores of a softmax stay in shared memory for the weights.
 #pragma once
 #include "router.cuh"
 
 namespace moe {
+
+// 1 / d for d in [1, 512]: two Newton steps from the single-precision
+// reciprocal, 2^-23 -> 2^-46 -> the double's last place or two.
+__device__ __forceinline__ double route_rcp(double d) {
+  double y = static_cast<double>(__frcp_rn(static_cast<float>(d)));
+  y = fma(y, fma(-d, y, 1.0), y);
+  return fma(y, fma(-d, y, 1.0), y);
+}
+
+// sigmoid(l) = 1 / (1 + a) or a / (1 + a) with a = exp(-|l|) in (0, 1]
+__device__ __forceinline__ double route_sigmoid(float l) {
+  const double a = exp(-fabs(static_cast<double>(l)));
+  const double r = route_rcp(1.0 + a);
+  return l < 0.f ? a * r : r;
+}
+
+// Lanes that share a group in the group choice: 32 / (n_group rounded up to a
+// power of two); the group's values lie `stride` words apart in shared memory,
+// with stride % 32 == lanes so that the 32 lanes read 32 banks.
+struct RouteGroups {
+  int size, lanes, stride;
+  uint32_t magic;  // expert e is in group e * magic >> 20: exact for e < 512, since magic exceeds 2^20 / size by
+                   // less than 1 and e / 2^20 stays below 1 / size, the least distance to the next quotient
+  RouteGroups() = default;
+  __host__ RouteGroups(int E, int n_group) {
+    int p = 1;
+    while (p < n_group) p *= 2;
+    size = E / n_group;
+    lanes = 32 / p;
+    stride = size + ((lanes - size) % 32 + 32) % 32;
+    magic = ((1u << 20) + size - 1) / size;
+  }
+  __host__ __device__ int words(int n_group) const { return n_group * stride; }
+};
 
 struct RouteArgs {
   const void* logits;  // [T, E], rows ld apart
@@ -39,6 +75,7 @@ struct RouteArgs {
   float rsf;
   int32_t* ids;  // [T, k]
   float* wts;    // [T, k]
+  RouteGroups groups;
 };
 
 constexpr int kRouteWarps = 4;
@@ -62,28 +99,29 @@ __device__ __forceinline__ double route_exp(float l, float mx) {
   return l == mx ? 1.0 : exp(static_cast<double>(l) - static_cast<double>(mx));
 }
 
-// Lanes that share a group in the group choice: 32 / (n_group rounded up to a
-// power of two); the group's values lie `stride` words apart in shared memory,
-// with stride % 32 == lanes so that the 32 lanes read 32 banks.
-struct RouteGroups {
-  int size, lanes, stride;
-  __host__ __device__ RouteGroups(int E, int n_group) {
-    int p = 1;
-    while (p < n_group) p *= 2;
-    size = E / n_group;
-    lanes = 32 / p;
-    stride = size + ((lanes - size) % 32 + 32) % 32;
-  }
-  __host__ __device__ size_t smem_words(int n_group) const { return static_cast<size_t>(n_group) * stride; }
-};
-
 template <int VPL, bool SOFTMAX>
 __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
   extern __shared__ float route_sm[];  // per warp: c by group (n_group > 1)
+  __shared__ double p_sm[SOFTMAX ? kRouteWarps : 1][SOFTMAX ? 32 * VPL : 1];
   const int wib = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * kRouteWarps + wib;
   if (t >= a.T) return;
+  const float NEG_INF = __int_as_float(0xff800000);
+  const size_t row = static_cast<size_t>(t) * a.ld;
+
+  // every load of the row's inputs first: they are in flight together
+  float l[VPL], bias[VPL];
+  float mx = NEG_INF;
+  bool on[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane + 32 * i;
+    const bool in = e < a.E;
+    l[i] = in ? route_logit(a, row, e) : NEG_INF;
+    on[i] = !(in && a.mask) || __ldg(a.mask + e) != 0;
+    bias[i] = in && a.bias ? __ldg(a.bias + e) : 0.f;
+  }
   const size_t out = static_cast<size_t>(t) * a.k + lane;
   if (a.num_valid && t >= __ldg(a.num_valid)) {
     if (lane < a.k) {
@@ -92,24 +130,16 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
     }
     return;
   }
-  const float NEG_INF = __int_as_float(0xff800000);
-  const size_t row = static_cast<size_t>(t) * a.ld;
-
-  // scores of this lane's experts e = lane + 32 i
-  float l[VPL];
-  float mx = NEG_INF;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    const int e = lane + 32 * i;
-    l[i] = NEG_INF;
-    if (e < a.E && !(a.mask && __ldg(a.mask + e) == 0)) {
-      const float v = route_logit(a, row, e);
-      if (v == v) l[i] = v;
-    }
+    if (!on[i] || l[i] != l[i]) l[i] = NEG_INF;
     mx = fmaxf(mx, l[i]);
   }
+
+  // c of this lane's experts e = lane + 32 i, then its key; positions past E
+  // take no part (key 0)
   double inv_z = 1.0;
-  uint32_t key[VPL];
+  float c[VPL];
   if (SOFTMAX) {
     mx = warp_max_f(mx);
     double p[VPL];
@@ -117,32 +147,31 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       p[i] = l[i] == NEG_INF ? 0.0 : route_exp(l[i], mx);
+      p_sm[wib][lane + 32 * i] = p[i];
       z += p[i];
     }
     z = warp_sum_d(z);
-    inv_z = z > 0.0 ? 1.0 / z : 0.0;
+    inv_z = z > 0.0 ? route_rcp(z) : 0.0;  // the largest term is 1
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = __float_as_uint(static_cast<float>(p[i] * inv_z));
+    for (int i = 0; i < VPL; ++i) c[i] = static_cast<float>(p[i] * inv_z);
   } else {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      key[i] = __float_as_uint(static_cast<float>(1.0 / (1.0 + exp(-static_cast<double>(l[i])))));
+    for (int i = 0; i < VPL; ++i) c[i] = static_cast<float>(route_sigmoid(l[i]));
   }
-  // c, then its key; positions past E take no part (key 0)
-  const RouteGroups G(a.E, a.n_group);
-  float* c_sm = route_sm + static_cast<size_t>(wib) * G.smem_words(a.n_group);
+  const RouteGroups& G = a.groups;
+  float* c_sm = route_sm + wib * G.words(a.n_group);
+  uint32_t key[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = lane + 32 * i;
-    float c = __uint_as_float(key[i]);
     key[i] = 0;
     if (e < a.E) {
-      if (a.bias) c = __fadd_rn(c, __ldg(a.bias + e));
-      if (l[i] == NEG_INF || c != c) c = NEG_INF;
-      key[i] = order_key(c);
+      float v = a.bias ? __fadd_rn(c[i], bias[i]) : c[i];
+      if (l[i] == NEG_INF || v != v) v = NEG_INF;
+      key[i] = order_key(v);
       if (a.n_group > 1) {
-        const int g = e / G.size;
-        c_sm[g * G.stride + (e - g * G.size)] = c;
+        const int g = static_cast<int>(static_cast<uint32_t>(e) * G.magic >> 20);
+        c_sm[e + g * (G.stride - G.size)] = v;
       }
     }
   }
@@ -179,7 +208,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const int e = lane + 32 * i;
-      if (e < a.E && !((kept >> (e / G.size)) & 1u)) key[i] = 0;
+      if (!((kept >> (static_cast<uint32_t>(e) * G.magic >> 20)) & 1u)) key[i] = 0;  // past E the key is 0 already
     }
   }
 
@@ -193,6 +222,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
       best = key[i];
       bi = i;
     }
+  __syncwarp();  // p_sm
   int sel = 0;
   bool live = false;
   for (int j = 0; j < a.k; ++j) {
@@ -219,8 +249,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
 
   double p = 0.0;
   if (lane < a.k && live) {
-    const float v = route_logit(a, row, sel);
-    p = SOFTMAX ? route_exp(v, mx) * inv_z : 1.0 / (1.0 + exp(-static_cast<double>(v)));
+    p = SOFTMAX ? p_sm[wib][sel] * inv_z : route_sigmoid(route_logit(a, row, sel));
   }
   if (a.renormalize) {
     const double sum = warp_sum_d(p);

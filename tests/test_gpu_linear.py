@@ -129,7 +129,12 @@ SHAPES = [(1, 1, 8), (1, 128, 64), (1, 2048, 2048), (2, 129, 72), (15, 127, 136)
           (31, 33, 520), (32, 7168, 256), (33, 640, 2048), (63, 65, 4096), (64, 1000, 264), (65, 384, 1032),
           (127, 255, 128), (128, 128, 7168), (129, 257, 192), (255, 1409, 320), (256, 512, 2816), (257, 130, 640),
           (300, 2815, 408), (511, 768, 1408), (513, 77, 2056), (1000, 1000, 1000), (1024, 512, 16), (2049, 384, 200),
-          (4096, 256, 512), (1, 20000, 64), (4097, 8, 64)]
+          (4096, 256, 512), (1, 20000, 64), (4097, 8, 64),
+          # more than 64 tokens: K over 4 and 2 pairs of a cluster, with one and two accumulations, tails of every
+          # kind, and tiles of every width on the way to whole waves
+          (66, 256, 7168), (129, 512, 4096), (200, 250, 4104), (257, 97, 3600), (700, 150, 6664), (1000, 256, 7168),
+          (100, 2048, 7168), (400, 1030, 5000), (512, 512, 4096), (300, 7168, 520), (2000, 1500, 264),
+          (1500, 2300, 72), (3000, 1700, 136), (4096, 2048, 96), (2304, 4400, 64)]
 
 
 @pytest.mark.parametrize("T,N,K", SHAPES)
@@ -160,6 +165,8 @@ def test_linear_random(cuda_lib, act, T, N, K, dt, odt):
 
 
 @pytest.mark.parametrize("T,N,K,dt,odt", [(1, 2048, 7168, "bf16", "f32"), (4096, 256, 7168, "bf16", "f32"),
+                                          (40, 1000, 7168, "fp16", "f32"), (100, 256, 7168, "bf16", "f32"),
+                                          (900, 512, 7168, "fp8", "f32"), (2000, 2816, 4096, "bf16", "f32"),
                                           (777, 2815, 4096, "fp16", "fp16"), (1024, 5632, 4096, "fp8", "bf16")])
 def test_linear_long_k(cuda_lib, T, N, K, dt, odt):
     _check(T, N, K, dt, odt, bias="bf16", pad=8 if dt != "fp8" else 16)
@@ -188,6 +195,24 @@ def test_linear_infinities_and_nan(cuda_lib, T, N, K):
         got = out.cpu()
         assert torch.equal(torch.isnan(got), torch.isnan(ref)), act
         assert torch.equal(got[torch.isinf(ref)], ref[torch.isinf(ref)]), act
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 256, 7168), (40, 1000, 7168), (100, 256, 7168), (300, 2048, 7168),
+                                   (4096, 256, 7168), (2000, 2816, 4096)])
+def test_linear_fp32_results_keep_precision(cuda_lib, T, N, K):
+    """fp32 results sum pieces of at most 14 K atoms (896 values) of the tensor
+    core's accumulation in fp32: an accumulation over L values, each addition
+    cutting the sum to 24 bits (an error below 2^-23 of it, of one sign), is off
+    by less than 2^-23 (L / 16) / 2 of its size on average, pieces add with
+    independent signs like their values do, so the 2-norm error stays below
+    2^-23 * 28 = 3.4e-6 relative; in fact it is below 1e-6."""
+    g = torch.Generator().manual_seed(T + N)
+    x = torch.randn((T, K), generator=g).to(torch.bfloat16).cuda()
+    w = (torch.randn((N, K), generator=g) * 0.05).to(torch.bfloat16).cuda()
+    out = torch.empty((T, N), device="cuda")
+    capi.moe_linear(capi.MOE_DT_BF16, x, None, w, None, None, 0, None, out)
+    ref = x.double() @ w.double().t()
+    assert (out.double() - ref).norm() <= 3.4e-6 * ref.norm()
 
 
 def test_linear_no_rows(cuda_lib):

@@ -144,6 +144,21 @@ def test_norm_infinities_and_nan(cuda_lib):
     assert torch.isfinite(y[2:]).all() and torch.isfinite(c[2:]).all()
 
 
+def test_norm_fp8_tiny_scale(cuda_lib):
+    """A row whose scale is subnormal still gets finite codes: 448 for its
+    amax (the quotient amax / (amax / 448) with the subnormal scale's own
+    rounding, half a step of 2^-149 in about 2^-129) and 0 for zeros."""
+    H = 64
+    x = torch.ones((2, H), dtype=torch.bfloat16, device="cuda")
+    x[:, 1] = 0
+    gamma = torch.full((H,), 1e-36, dtype=torch.float32, device="cuda")
+    c, s = torch.empty((2, H), dtype=torch.uint8, device="cuda"), torch.empty(2, device="cuda")
+    capi.moe_rmsnorm_quantize(QUANT["fp8"], x, None, gamma, 1e-6, None, None, c, s)
+    torch.cuda.synchronize()
+    v = c.cpu().view(torch.float8_e4m3fn).float()
+    assert torch.all(v[:, 1] == 0) and torch.all(v[:, 2:] == 448) and torch.all(s > 0)
+
+
 def test_norm_matches_the_quantiser(cuda_lib):
     """With gamma such that y is exactly representable the codes and scales are
     those of moe_quantize_activations on the stored y."""
