@@ -232,28 +232,26 @@ _OPERAND_DT = {MOE_DT_BF16: (torch.bfloat16,), MOE_DT_FP16: (torch.float16,),
 _F32, _I32, _BYTES = (torch.float32,), (torch.int32,), (torch.uint8, torch.bool)
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
 # The wrappers below are called once per operator of a decode step, whose
 # kernels take a few microseconds: their checks are kept to attribute reads.
 
 
-def _device(*tensors):
+def _device(first, *others):
     """Index of the one device that every tensor lives on, the current one (the
     calls launch on its stream)."""
-    dev = -1
-    for t in tensors:
-        if t is not None:
-            d = t.get_device()
-            if d != dev:
-                if dev >= 0 or d < 0:
-                    raise ValueError("tensors must live on one CUDA device")
-                dev = d
-    if dev != torch._C._cuda_getDevice():
-        raise ValueError(f"tensors on cuda:{dev}, current device cuda:{torch._C._cuda_getDevice()}")
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors must live on one CUDA device")
+    if dev < 0 or dev != _current_device():
+        raise ValueError(f"tensors on {first.device}: they must live on the current CUDA device")
     return dev
 
 
 def _raw_stream(stream, dev):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return _current_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _rows(t, name, rows, cols, types):
@@ -263,13 +261,11 @@ def _rows(t, name, rows, cols, types):
     if t.shape != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
     ld, step = t.stride()
-    if step != 1 and cols > 1:
-        raise ValueError(f"the rows of {name} must be contiguous")
-    if rows > 1:
-        if ld < cols:
-            raise ValueError(f"the rows of {name} must not overlap")
-        return ld
-    return -(-cols // 16) * 16  # the stride of one row or none says nothing
+    if (step == 1 or cols == 1) and (rows == 1 or ld >= cols):
+        return ld if rows > 1 else -(-cols // 16) * 16  # the stride of a single row says nothing
+    if rows == 0:
+        return -(-cols // 16) * 16
+    raise ValueError(f"the rows of {name} must be contiguous and must not overlap")
 
 
 def _vec(t, name, n, types):

@@ -12,10 +12,44 @@ in ``libmoe_b200.so``.
 """
 from __future__ import annotations
 
+from dataclasses import dataclass
+
 import torch
 
 from . import capi
 from .configs import MoEConfig
+
+
+@dataclass
+class Routing:
+    """Routing of a layer through ``moe_route`` in place of ``moe_router_topk``:
+    either score with a balance bias, groups, experts switched off and padded
+    batches (``num_valid``: int32 [1] on the device; the rows behind it take no
+    expert and keep what ``layer.out`` held). The tensors are read at every
+    forward, captured graphs included."""
+    score: str = "softmax"             # 'softmax' | 'sigmoid'
+    n_group: int = 1
+    topk_group: int = 1
+    group_score: str = "top2"          # 'top2' | 'max'
+    renormalize: bool = True
+    rsf: float = 1.0
+    bias: torch.Tensor | None = None         # fp32 [E]
+    expert_mask: torch.Tensor | None = None  # uint8 [E], 0 = off
+    num_valid: torch.Tensor | None = None    # int32 [1]
+
+
+def route_tokens(cfg: MoEConfig, inp: dict, routing: Routing | None, topk_ids, topk_weights, stream):
+    """The routing step of a layer, from ``inp["logits"]``: the config's own
+    (``moe_router_topk``) or a ``Routing`` (``moe_route``)."""
+    if routing is None:
+        mode = capi.MOE_ROUTE_SOFTMAX if cfg.route == "softmax" else capi.MOE_ROUTE_GROUPED_SIGMOID
+        capi.moe_router_topk(inp["logits"], inp.get("correction_bias"), cfg.top_k, mode, cfg.n_group, cfg.topk_group,
+                             cfg.renormalize, cfg.rsf, topk_ids, topk_weights, stream)
+        return
+    r = routing
+    capi.moe_route(inp["logits"], r.bias, r.expert_mask, r.num_valid, cfg.top_k, capi.SCORES[r.score], r.n_group,
+                   r.topk_group, capi.GROUP_SCORES[r.group_score], r.renormalize, r.rsf, topk_ids, topk_weights,
+                   stream)
 
 
 def capture_forward(layer, stream=None, steps: int = 1) -> torch.cuda.CUDAGraph:
@@ -49,12 +83,16 @@ class MoELayer:
     ``self.logits``. With ``quantize_x`` (fp8 / MXFP8 layers) the step starts
     from the bf16 activations ``x_r``: ``moe_quantize_activations`` writes
     ``self.xq`` / ``self.xq_scale``, which both GEMM paths then read instead
-    of ``x`` / ``x_scale``.
+    of ``x`` / ``x_scale``. With ``routing`` the experts are chosen by
+    ``moe_route`` (see ``Routing``) instead of the config's routing mode.
     """
 
     def __init__(self, cfg: MoEConfig, inp: dict, block_m: int | None = None, device=None,
-                 router_gemm: bool = False, quantize_x: bool = False):
+                 router_gemm: bool = False, quantize_x: bool = False, routing: Routing | None = None):
         self.cfg = cfg
+        if routing is not None and router_gemm:
+            raise ValueError("router_gemm routes by the config's mode: give it or a Routing")
+        self.routing = routing
         self.router_gemm = router_gemm
         if quantize_x and cfg.dtype == "bf16":
             raise ValueError("quantize_x applies to the fp8 and MXFP8 layers")
@@ -149,14 +187,13 @@ class MoELayer:
         microseconds inside a CUDA graph; time whole steps without them.)"""
         cfg, inp = self.cfg, self.inp
         T, H, E, k, I = cfg.T, cfg.H, cfg.E, cfg.top_k, cfg.I
-        mode = capi.MOE_ROUTE_SOFTMAX if cfg.route == "softmax" else capi.MOE_ROUTE_GROUPED_SIGMOID
         if self.router_gemm:
+            mode = capi.MOE_ROUTE_SOFTMAX if cfg.route == "softmax" else capi.MOE_ROUTE_GROUPED_SIGMOID
             capi.moe_router_gemm_topk(inp["x_r"], inp["w_r"], inp["logit_bias"], inp.get("correction_bias"), k,
                                       mode, cfg.n_group, cfg.topk_group, cfg.renormalize, cfg.rsf, self.logits,
                                       self.topk_ids, self.topk_weights, stream)
         else:
-            capi.moe_router_topk(inp["logits"], inp.get("correction_bias"), k, mode, cfg.n_group, cfg.topk_group,
-                                 cfg.renormalize, cfg.rsf, self.topk_ids, self.topk_weights, stream)
+            route_tokens(cfg, inp, self.routing, self.topk_ids, self.topk_weights, stream)
         capi.moe_align_sort(self.topk_ids, E, self.bm, self.sorted_ids, self.block_expert, self.expert_counts,
                             self.expert_offsets, self.num_padded, stream)
         if wait_x is not None:  # the quantised activations (forward with quantize_x)
@@ -225,11 +262,13 @@ class FusedSharedMoELayer:
     zero-padded past Is, with the shared expert's weight scales. All k + m
     contributions meet in stage 2's fp32 workspace before the one bf16
     rounding: no addend, no side stream, no event. Same interface as MoELayer
-    (``forward``, ``out``, ``topk_ids``, ``topk_weights``).
+    (``forward``, ``out``, ``topk_ids``, ``topk_weights``, ``routing``).
     """
 
-    def __init__(self, cfg: MoEConfig, inp: dict, block_m: int | None = None, device=None):
+    def __init__(self, cfg: MoEConfig, inp: dict, block_m: int | None = None, device=None,
+                 routing: Routing | None = None):
         self.cfg = cfg
+        self.routing = routing
         self.inp = inp
         self.device = torch.device(device or inp["x"].device)
         dev = self.device
@@ -304,11 +343,9 @@ class FusedSharedMoELayer:
         cfg, inp = self.cfg, self.inp
         T, H, E, k, I = cfg.T, cfg.H, cfg.E, cfg.top_k, cfg.I
         s = stream or torch.cuda.current_stream(self.device)
-        mode = capi.MOE_ROUTE_SOFTMAX if cfg.route == "softmax" else capi.MOE_ROUTE_GROUPED_SIGMOID
         if self.gate is not None:
             capi.shared_expert_gate_dot(capi.MOE_DT_BF16, inp["x"], inp["w_gate"], True, self.gate, s)
-        capi.moe_router_topk(inp["logits"], inp.get("correction_bias"), k, mode, cfg.n_group, cfg.topk_group,
-                             cfg.renormalize, cfg.rsf, self.topk_ids, self.topk_weights, s)
+        route_tokens(cfg, inp, self.routing, self.topk_ids, self.topk_weights, s)
         capi.moe_append_shared_slots(self.topk_ids, self.topk_weights, E, self.m, self.gate, self.ids2,
                                      self.w2slots, s)
         capi.moe_align_sort(self.ids2, self.E2, self.bm, self.sorted_ids, self.block_expert, self.expert_counts,

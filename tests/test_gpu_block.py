@@ -1,0 +1,187 @@
+"""MoEBlock: projection with residual, norm with quantisation, router linear,
+general routing and the layer, run as a decoder block runs them. Every step is
+checked against the formula in 64 bits on the inputs the GPU gave it (the
+tolerances of the single operators' tests), the layer's output against the
+oracle on the same operands."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from gpu_helpers import BF16_TOL, FP8_TOL, assert_close_rms, check_routing
+from routed_shared_experts_b200 import capi, configs, synth
+from routed_shared_experts_b200.block import MoEBlock
+from routed_shared_experts_b200.layer import FusedSharedMoELayer, MoELayer, Routing
+
+pytestmark = pytest.mark.gpu
+EPS = 1e-6
+
+
+def _make(cfg, kind=MoELayer, A=320, attn_fp8=False, routing=None, seed=7):
+    inp = synth.make_layer_inputs(cfg)
+    dev = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in inp.items()}
+    g = torch.Generator().manual_seed(seed)
+    randn = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    attn, w_o = randn(cfg.T, A), randn(cfg.H, A) * 0.05
+    w = {"gamma": (1 + 0.1 * randn(cfg.H)).bfloat16().cuda(), "w_r": (randn(cfg.E, cfg.H) * 0.05).bfloat16().cuda(),
+         "logit_bias": (randn(cfg.E) * 0.1).cuda()}
+    scale = None
+    if attn_fp8:
+        ac, scale = synth.quant_fp8_rows(attn, 1)
+        wc, ws = synth.quant_fp8_rows(w_o, 1)
+        attn, scale, w["w_o"], w["w_o_scale"] = ac.cuda(), scale.cuda(), wc.cuda(), ws.cuda()
+    else:
+        attn, w["w_o"] = attn.bfloat16().cuda(), w_o.bfloat16().cuda()
+    residual = randn(cfg.T, cfg.H).bfloat16().cuda()
+    layer = kind(cfg, dev, routing=routing)
+    return MoEBlock(layer, w, attn, residual, attn_scale=scale, eps=EPS)
+
+
+def _check_front(block, res0):
+    """Projection, norm, quantisation and logits of the last forward."""
+    w, inp = block.w, block.layer.inp
+    f8 = lambda t: t.view(torch.float8_e4m3fn).double()  # noqa: E731
+    if block.attn_scale is None:
+        a, wo = block.attn.double(), w["w_o"].double()
+    else:
+        a = f8(block.attn) * block.attn_scale.double()[:, None]
+        wo = f8(w["w_o"]) * w["w_o_scale"].double()[:, None]
+    ref = a @ wo.t() + res0.double()
+    mag = a.abs() @ wo.abs().t()
+    res = block.residual.double()
+    K = a.shape[1]
+    assert torch.all((res - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -23 * (K / 8 + 8) * mag + 2.0 ** -22 * ref.abs())
+    y = res * torch.rsqrt((res * res).mean(1, keepdim=True) + EPS) * w["gamma"].double()
+    yb = block.y.double()
+    assert torch.all((yb - y).abs() <= (2.0 ** -8 + 2.0 ** -17) * y.abs())
+    if block.quant is not None:
+        c = f8(inp["x"])
+        s = (inp["x_scale"].double()[:, None] if block.quant == capi.MOE_DT_FP8_E4M3 else
+             torch.exp2(inp["x_scale"].double() - 127).repeat_interleave(32, 1))
+        v = (y / s).clamp(-448, 448)
+        assert torch.all((c - v).abs() <= 2.0 ** -4 * v.abs() + 2.0 ** -10 + 2.0 ** -17 * v.abs() + 2.0 ** -19)
+    wr = w["w_r"].double()
+    lref = yb @ wr.t() + w["logit_bias"].double()
+    lmag = yb.abs() @ wr.abs().t()
+    H = yb.shape[1]
+    assert torch.all((inp["logits"].double() - lref).abs() <= 2.0 ** -23 * (H / 8 + 8) * lmag + 2.0 ** -22 * lref.abs())
+
+
+def _oracle_view(block):
+    """The layer's operands as the block left them, on the host."""
+    return synth.oracle_view({k: (v.cpu() if isinstance(v, torch.Tensor) else v) for k, v in block.layer.inp.items()})
+
+
+def _check_layer(block, rows, fused):
+    cfg, layer = block.layer.cfg, block.layer
+    view = _oracle_view(block)
+    bias = None if view.get("correction_bias") is None else np.asarray(view["correction_bias"])
+    logits = np.asarray(view["logits"])
+    agree = check_routing(cfg, logits, bias, layer.topk_ids.cpu().numpy(), layer.topk_weights.cpu().numpy()) \
+        if rows == cfg.T else np.arange(rows)
+    ref = oracle.moe_layer(cfg.as_dict(), view, tokens=agree, shared_fused=fused)
+    tol = BF16_TOL if cfg.dtype == "bf16" else FP8_TOL
+    assert_close_rms(layer.out.float().cpu().numpy()[agree], ref["out"], tol, "out", rounded=[ref["out"]])
+
+
+CASES = [
+    (configs.DECODE_BF16, dict(T=48, H=512, E=16, top_k=4, I=128, Is=128), MoELayer, False),
+    (configs.DECODE_BF16, dict(T=48, H=512, E=16, top_k=4, I=128, Is=320), FusedSharedMoELayer, True),
+    (configs.FP8_A8W8, dict(T=100, H=512, E=16, top_k=4, I=256, Is=512, n_group=4, topk_group=2, block_m=32), MoELayer,
+     True),
+    (configs.MXFP8_PREFILL, dict(T=300, H=512, E=8, top_k=2, I=256, Is=256, n_group=4, topk_group=2), MoELayer, False),
+    (configs.MXFP8_PREFILL, dict(T=1, H=512, E=8, top_k=2, I=256, Is=256, n_group=4, topk_group=2, block_m=16),
+     FusedSharedMoELayer, False),
+]
+
+
+def _cfg(base, kw, name):
+    return configs.small(base, name=name, seed=61, **kw)
+
+
+def _routing(cfg, dev_bias=None, **kw):
+    """The config's own routing, through moe_route."""
+    score = "softmax" if cfg.route == "softmax" else "sigmoid"
+    return Routing(score=score, n_group=cfg.n_group, topk_group=cfg.topk_group, renormalize=cfg.renormalize,
+                   rsf=cfg.rsf, bias=dev_bias, **kw)
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+@pytest.mark.parametrize("general", [False, True])
+def test_block(cuda_lib, case, general):
+    base, kw, kind, attn_fp8 = CASES[case]
+    cfg = _cfg(base, kw, f"block{case}")
+    block = _make(cfg, kind, attn_fp8=attn_fp8)
+    if general:
+        block.layer.routing = _routing(cfg, block.layer.inp.get("correction_bias"))
+    res0 = block.residual.clone()
+    block.forward()
+    torch.cuda.synchronize()
+    assert capi.device_error() == 0
+    _check_front(block, res0)
+    _check_layer(block, cfg.T, kind is FusedSharedMoELayer)
+    assert torch.count_nonzero(block.layer.acc_ws).item() == 0
+
+
+@pytest.mark.parametrize("case", [0, 1, 2, 3])
+def test_block_padded_batches_from_one_graph(cuda_lib, case):
+    """One captured graph serves batches of every length: the rows behind
+    num_valid take no expert, keep what the output held, and leave the
+    workspaces as the next replay needs them."""
+    base, kw, kind, attn_fp8 = CASES[case]
+    cfg = _cfg(base, kw, f"padded{case}")
+    nv = torch.tensor([cfg.T], dtype=torch.int32, device="cuda")
+    block = _make(cfg, kind, attn_fp8=attn_fp8)
+    block.layer.routing = _routing(cfg, block.layer.inp.get("correction_bias"), num_valid=nv)
+    res0 = block.residual.clone()
+    block.forward()  # the first call outside a capture
+    torch.cuda.synchronize()
+    graph = block.capture(torch.cuda.Stream())
+    for n in (cfg.T // 3, 0, cfg.T, 1):
+        block.residual.copy_(res0)
+        block.layer.out.fill_(13.0)
+        nv.fill_(n)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert capi.device_error() == 0
+        assert torch.all(block.layer.topk_ids[n:] == capi.MOE_NO_EXPERT)
+        assert torch.all(block.layer.out[n:] == 13.0)
+        assert torch.count_nonzero(block.layer.acc_ws).item() == 0
+        _check_front(block, res0)
+        if n:
+            _check_layer(block, n, kind is FusedSharedMoELayer)
+
+
+def test_block_experts_switched_off(cuda_lib):
+    """Two experts left for four picks: the others carry weight 0 and the
+    layer's arrival counts stay whole."""
+    cfg = _cfg(configs.DECODE_BF16, dict(T=40, H=512, E=16, top_k=4, I=128, Is=128), "off")
+    mask = torch.zeros(cfg.E, dtype=torch.uint8, device="cuda")
+    mask[3] = mask[11] = 1
+    block = _make(cfg, routing=Routing(expert_mask=mask))
+    block.forward()
+    torch.cuda.synchronize()
+    assert capi.device_error() == 0
+    ids, w = block.layer.topk_ids.cpu(), block.layer.topk_weights.cpu()
+    assert torch.all(torch.sort(ids[:, :2], 1).values == torch.tensor([3, 11])) and torch.all(w[:, 2:] == 0)
+    assert ids[:, 2:].tolist() == [[0, 1]] * cfg.T
+    assert torch.count_nonzero(block.layer.acc_ws).item() == 0
+    # the same layer with top_k = 2 and only those two experts' logits
+    view = _oracle_view(block)
+    logits = np.asarray(view["logits"]).copy()
+    keep = np.zeros(cfg.E, bool)
+    keep[[3, 11]] = True
+    logits[:, ~keep] = -1e30
+    view["logits"] = torch.from_numpy(logits)
+    two = configs.small(cfg, top_k=2)
+    ref = oracle.moe_layer(two.as_dict(), view)
+    assert_close_rms(block.layer.out.float().cpu().numpy(), ref["out"], BF16_TOL, "out", rounded=[ref["out"]])
+
+
+def test_block_refusals(cuda_lib):
+    cfg = _cfg(configs.DECODE_BF16, dict(T=8, H=512, E=16, top_k=4, I=128, Is=128), "refuse")
+    inp = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in synth.make_layer_inputs(cfg).items()}
+    with pytest.raises(ValueError):
+        MoELayer(cfg, inp, router_gemm=True, routing=Routing())
+    with pytest.raises(ValueError):
+        MoEBlock(MoELayer(cfg, inp, router_gemm=True), {}, None, None)
