@@ -26,6 +26,8 @@
 // bytes, which needs all SMs pulling at once; the K split is what supplies them
 // when N / 128 tiles are fewer than the SMs.
 #pragma once
+#include <type_traits>
+
 #include "gemm.cuh"
 #include "norm.cuh"
 #include "router.cuh"
@@ -55,7 +57,7 @@ struct LinearArgs {
   int n_tb;    // token blocks (k_linear_split) or 256-token tiles (k_linear_tile)
   int tn, n_nt;  // k_linear_tile: outputs per tile (a multiple of 32, at most 256), tiles along N
   int split;     // k_linear_tile with SPLIT: pairs along K
-  int out_vec, res_vec;  // k_linear_tile: rows allow 16-byte accesses
+  int out_unit, res_unit;  // k_linear_tile: bytes that divide every row's address and length: 16, 4 or 2
 };
 
 // Instruction descriptor of kind::f16 with both operands bf16 or both fp16.
@@ -415,7 +417,7 @@ __global__ void __launch_bounds__(kSplitThreads)
 // accumulator.
 
 constexpr int kTileEpiWarps = 8;
-constexpr int kTileThreads = 128 + 32 * kTileEpiWarps;
+constexpr int kTileThreads = 96 + 32 * kTileEpiWarps;  // two producers, MMA, epilogue
 constexpr int kPromoteAtoms = 8;
 constexpr int kPromoteTn = 128;  // outputs per tile with PROMOTE: 64 running sums per epilogue thread
 
@@ -441,65 +443,120 @@ struct TileCfg {
 // XOR spreads both the row-wise and the row-group-wise accesses over all banks.
 __device__ __forceinline__ int stage_off(int r, int u) { return r * 64 + ((u ^ ((r >> 1) & 3)) << 4); }
 
-// 64 bytes of each of the rows row0.. of a [T, N] matrix from column n0, as the
-// warp's lanes hold them: 8 rows x 4 units per register.
-template <typename TE>
-__device__ __forceinline__ void fetch_rows(uint4 (&v)[4], const TE* src, size_t ld, int row0, int T, int n0, int lane) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = i * 8 + (lane >> 2);
-    v[i] = row0 + r < T ? *reinterpret_cast<const uint4*>(src + (row0 + r) * ld + n0 + (lane & 3) * (16 / sizeof(TE)))
-                        : make_uint4(0, 0, 0, 0);
-  }
-}
-
-__device__ __forceinline__ void stage_put(uint8_t* st, const uint4 (&v)[4], int lane) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(st + stage_off(i * 8 + (lane >> 2), lane & 3)) = v[i];
-}
-
-// The same rows into the staging value by value: unaligned rows, or `cols`
-// columns at the end of the matrix.
-template <typename TE>
-__device__ __forceinline__ void stage_load_cols(uint8_t* st, const TE* src, size_t ld, int row0, int T, int n0,
-                                                int cols, int lane) {
-  if (lane < cols) {
-    const int b = lane * static_cast<int>(sizeof(TE));
-#pragma unroll 8
-    for (int r = 0; r < 32; ++r)
-      if (row0 + r < T) *reinterpret_cast<TE*>(st + stage_off(r, b >> 4) + (b & 15)) = src[(row0 + r) * ld + n0 + lane];
-  }
-}
-
-template <typename TE>
-__device__ __forceinline__ void stage_store(const uint8_t* st, TE* dst, size_t ld, int row0, int T, int n0, int cols,
-                                            bool vec, int lane) {
-  if (vec) {
+// A warp's copies between 32 rows of a matrix, 64 bytes each (`bytes` of them
+// valid, `rows` rows valid), and its staging, in units of U = 16, 4 or 2 bytes:
+// 64 / U lanes take a row, so a copy instruction moves whole row segments
+// whatever their alignment. Register w of a lane holds, for U = 16, word w % 4
+// of the unit of row 8 (w / 4) + lane / 4; for U = 4, row 2 w + lane / 16; for
+// U = 2, rows 2 w and 2 w + 1.
+template <int U>
+__device__ __forceinline__ void fetch_rows(uint32_t (&v)[16], const uint8_t* src, size_t ld, int rows, int bytes,
+                                           int lane) {
+  if constexpr (U == 16) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = i * 8 + (lane >> 2);
-      if (row0 + r < T)
-        *reinterpret_cast<uint4*>(dst + (row0 + r) * ld + n0 + (lane & 3) * (16 / sizeof(TE))) =
-            *reinterpret_cast<const uint4*>(st + stage_off(r, lane & 3));
+      const int r = 8 * i + (lane >> 2), at = (lane & 3) * 16;
+      uint4 f = make_uint4(0, 0, 0, 0);
+      if (r < rows && at < bytes) f = *reinterpret_cast<const uint4*>(src + r * ld + at);
+      v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
     }
-  } else if (lane < cols) {
-    const int b = lane * static_cast<int>(sizeof(TE));
-#pragma unroll 8
-    for (int r = 0; r < 32; ++r)
-      if (row0 + r < T) dst[(row0 + r) * ld + n0 + lane] = *reinterpret_cast<const TE*>(st + stage_off(r, b >> 4) + (b & 15));
+  } else if constexpr (U == 4) {
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      const int r = 2 * w + (lane >> 4), at = (lane & 15) * 4;
+      v[w] = r < rows && at < bytes ? *reinterpret_cast<const uint32_t*>(src + r * ld + at) : 0u;
+    }
+  } else {
+    uint32_t h[32];
+    if (rows >= 32 && bytes == 64) {  // without conditions the loads go out together
+#pragma unroll
+      for (int r = 0; r < 32; ++r) h[r] = *reinterpret_cast<const unsigned short*>(src + r * ld + 2 * lane);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 32; ++r)
+        h[r] = r < rows && 2 * lane < bytes ? *reinterpret_cast<const unsigned short*>(src + r * ld + 2 * lane) : 0u;
+    }
+#pragma unroll
+    for (int w = 0; w < 16; ++w) v[w] = h[2 * w] | (h[2 * w + 1] << 16);
   }
+}
+
+template <int U>
+__device__ __forceinline__ void stage_put(uint8_t* st, const uint32_t (&v)[16], int lane) {
+  if constexpr (U == 16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint4*>(st + stage_off(8 * i + (lane >> 2), lane & 3)) =
+          make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else if constexpr (U == 4) {
+#pragma unroll
+    for (int w = 0; w < 16; ++w)
+      *reinterpret_cast<uint32_t*>(st + stage_off(2 * w + (lane >> 4), (lane & 15) >> 2) + (lane & 3) * 4) = v[w];
+  } else {
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      const int in = (lane & 7) * 2;
+      *reinterpret_cast<unsigned short*>(st + stage_off(2 * w, lane >> 3) + in) = static_cast<unsigned short>(v[w]);
+      *reinterpret_cast<unsigned short*>(st + stage_off(2 * w + 1, lane >> 3) + in) =
+          static_cast<unsigned short>(v[w] >> 16);
+    }
+  }
+}
+
+template <int U>
+__device__ __forceinline__ void stage_store(const uint8_t* st, uint8_t* dst, size_t ld, int rows, int bytes, int lane) {
+  constexpr int kLanes = 64 / U, kRows = 32 / kLanes;  // lanes per row, rows per instruction
+  using TU = std::conditional_t<U == 16, uint4, std::conditional_t<U == 4, uint32_t, unsigned short>>;
+  const int at = lane % kLanes * U, r0 = lane / kLanes;
+  TU v[kLanes];  // all read before any is stored
+#pragma unroll
+  for (int i = 0; i < kLanes; ++i)
+    v[i] = *reinterpret_cast<const TU*>(st + stage_off(kRows * i + r0, at >> 4) + (at & 15));
+  dst += r0 * ld + at;
+  if (rows >= 32 && bytes == 64) {
+#pragma unroll
+    for (int i = 0; i < kLanes; ++i) *reinterpret_cast<TU*>(dst + kRows * i * ld) = v[i];
+  } else if (at < bytes) {
+#pragma unroll
+    for (int i = 0; i < kLanes; ++i)
+      if (kRows * i + r0 < rows) *reinterpret_cast<TU*>(dst + kRows * i * ld) = v[i];
+  }
+}
+
+// Residual rows of this warp from column n0 (64 bytes of each), by their unit.
+template <int OS, bool VEC>
+__device__ __forceinline__ void fetch_residual(const LinearArgs& g, uint32_t (&v)[16], int row0, int n0, int lane) {
+  const uint8_t* src = static_cast<const uint8_t*>(g.residual) + (row0 * g.ldr + n0) * OS;
+  const int bytes = min(64, (g.N - n0) * OS), rows = g.T - row0;
+  if (VEC || g.res_unit == 16) fetch_rows<16>(v, src, g.ldr * OS, rows, bytes, lane);
+  else if (OS == 4 || g.res_unit == 4) fetch_rows<4>(v, src, g.ldr * OS, rows, bytes, lane);
+  else fetch_rows<2>(v, src, g.ldr * OS, rows, bytes, lane);
+}
+
+template <int OS, bool VEC>
+__device__ __forceinline__ void put_residual(const LinearArgs& g, uint8_t* st, const uint32_t (&v)[16], int lane) {
+  if (VEC || g.res_unit == 16) stage_put<16>(st, v, lane);
+  else if (OS == 4 || g.res_unit == 4) stage_put<4>(st, v, lane);
+  else stage_put<2>(st, v, lane);
+}
+
+template <int OS, bool VEC>
+__device__ __forceinline__ void store_result(const LinearArgs& g, const uint8_t* st, int row0, int n0, int lane) {
+  uint8_t* dst = static_cast<uint8_t*>(g.out) + (row0 * g.ldo + n0) * OS;
+  const int bytes = min(64, (g.N - n0) * OS), rows = g.T - row0;
+  if (VEC || g.out_unit == 16) stage_store<16>(st, dst, g.ldo * OS, rows, bytes, lane);
+  else if (OS == 4 || g.out_unit == 4) stage_store<4>(st, dst, g.ldo * OS, rows, bytes, lane);
+  else stage_store<2>(st, dst, g.ldo * OS, rows, bytes, lane);
 }
 
 // Residual, rounding and store of 32 columns n0.. of this warp's 32 rows
 // (16-bit results): thread = row, through the staging. `res`: the residual
-// fetched ahead (fetch_rows), where whole 16-byte units could be.
-template <typename TX>
-__device__ __forceinline__ void tile_store_16(const LinearArgs& g, uint8_t* st, float (&v)[32], const uint4 (&res)[4],
-                                              int row0, int n0, int lane) {
-  const int cols = min(32, g.N - n0);
+// fetched ahead (fetch_residual).
+template <typename TX, bool VEC>
+__device__ __forceinline__ void tile_store_16(const LinearArgs& g, uint8_t* st, float (&v)[32],
+                                              const uint32_t (&res)[16], int row0, int n0, int lane) {
   if (g.residual) {
-    if (g.res_vec && cols == 32) stage_put(st, res, lane);
-    else stage_load_cols(st, static_cast<const TX*>(g.residual), g.ldr, row0, g.T, n0, cols, lane);
+    put_residual<2, VEC>(g, st, res, lane);
     __syncwarp();
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -515,27 +572,21 @@ __device__ __forceinline__ void tile_store_16(const LinearArgs& g, uint8_t* st, 
         make_uint4(pack2(v[8 * u], v[8 * u + 1], TX()), pack2(v[8 * u + 2], v[8 * u + 3], TX()),
                    pack2(v[8 * u + 4], v[8 * u + 5], TX()), pack2(v[8 * u + 6], v[8 * u + 7], TX()));
   __syncwarp();
-  stage_store(st, static_cast<TX*>(g.out), g.ldo, row0, g.T, n0, cols, g.out_vec && cols == 32, lane);
+  store_result<2, VEC>(g, st, row0, n0, lane);
   __syncwarp();  // the staging is rewritten next
 }
 
-// The same with fp32 results: two halves of 16 columns.
-__device__ __forceinline__ void tile_store_32(const LinearArgs& g, uint8_t* st, float (&v)[32], int row0, int n0,
-                                              int lane) {
+// The same with fp32 results: two halves of 16 columns (`res`: the first one's).
+template <bool VEC>
+__device__ __forceinline__ void tile_store_32(const LinearArgs& g, uint8_t* st, float (&v)[32], uint32_t (&res)[16],
+                                              int row0, int n0, int lane) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int c0 = n0 + 16 * h;
-    const int cols = min(16, g.N - c0);
-    if (cols <= 0) return;
+    if (c0 >= g.N) return;
     if (g.residual) {
-      const float* src = static_cast<const float*>(g.residual);
-      if (g.res_vec && cols == 16) {
-        uint4 res[4];
-        fetch_rows(res, src, g.ldr, row0, g.T, c0, lane);
-        stage_put(st, res, lane);
-      } else {
-        stage_load_cols(st, src, g.ldr, row0, g.T, c0, cols, lane);
-      }
+      put_residual<4, VEC>(g, st, res, lane);
+      if (h == 0 && c0 + 16 < g.N) fetch_residual<4, VEC>(g, res, row0, c0 + 16, lane);  // the second half, meanwhile
       __syncwarp();
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -551,7 +602,7 @@ __device__ __forceinline__ void tile_store_32(const LinearArgs& g, uint8_t* st, 
       *reinterpret_cast<float4*>(st + stage_off(lane, u)) =
           make_float4(v[16 * h + 4 * u], v[16 * h + 4 * u + 1], v[16 * h + 4 * u + 2], v[16 * h + 4 * u + 3]);
     __syncwarp();
-    stage_store(st, static_cast<float*>(g.out), g.ldo, row0, g.T, c0, cols, g.out_vec && cols == 16, lane);
+    store_result<4, VEC>(g, st, row0, c0, lane);
     __syncwarp();
   }
 }
@@ -584,7 +635,7 @@ __device__ __forceinline__ float4 ld_shared_cluster_f32x4(uint32_t cluster_addr)
 
 // Four consecutive values (`cols` of them valid) of the residual and the result.
 __device__ __forceinline__ void load_res4(const LinearArgs& g, size_t at, int cols, float (&res)[4]) {
-  if (g.res_vec && cols == 4) {
+  if (g.res_unit == 16 && cols == 4) {
     if (g.out_dt == 4) {
       const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(g.residual) + at);
       res[0] = f.x, res[1] = f.y, res[2] = f.z, res[3] = f.w;
@@ -606,7 +657,7 @@ __device__ __forceinline__ void load_res4(const LinearArgs& g, size_t at, int co
 }
 
 __device__ __forceinline__ void store4(const LinearArgs& g, size_t at, int cols, const float (&v)[4]) {
-  if (g.out_vec && cols == 4) {
+  if (g.out_unit == 16 && cols == 4) {
     if (g.out_dt == 4)
       *reinterpret_cast<float4*>(static_cast<float*>(g.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
     else if (g.out_dt == 0)
@@ -677,7 +728,8 @@ __device__ __forceinline__ void split_rows(const LinearArgs& g, uint32_t part, u
   }
 }
 
-template <bool FP8, bool PROMOTE, bool SPLIT>
+// VEC: every row of the result and of the residual allows 16-byte accesses.
+template <bool FP8, bool PROMOTE, bool SPLIT, bool VEC>
 __global__ void __launch_bounds__(kTileThreads, 1)
     k_linear_tile(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXt,
                   const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWt,
@@ -834,7 +886,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     }
     __syncwarp();
-  } else if (SPLIT && warp >= 4) {
+  } else if (SPLIT && warp >= 3) {
     // partial tile to shared memory: the stages are free once the last accumulation is complete
     const int q = warp & 3;
     const int r = 32 * q + lane;
@@ -844,7 +896,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (ok) {
       tc_fence_after();
       float4* part = reinterpret_cast<float4*>(stages);
-      for (int c = (warp - 4) >> 2; c < g.tn / 32; c += 2) {
+      for (int c = (warp - 3) >> 2; c < g.tn / 32; c += 2) {
         const uint32_t at = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(32 * c);
         float v[32];
         tmem_ld32(at, v);
@@ -861,9 +913,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           part[part_unit(r, 8 * c + i, g.tn)] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
       }
     }
-  } else if (!SPLIT && warp >= 4) {
-    const int ew = warp - 4;
-    const int q = ew & 3;     // TMEM lane quarter
+  } else if (!SPLIT && warp >= 3) {
+    const int ew = warp - 3;
+    const int q = warp & 3;    // TMEM lane quarter
     const int half = ew >> 2;  // columns 32 c.. with c % 2 == half
     uint8_t* st = smem + ew * L::kWarpOut;
     const uint32_t acc_empty0 = mapa_shared(smem_u32(acc_empty), leader);
@@ -880,14 +932,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
       // weight scale, bias and residual of chunk c, fetched a chunk ahead
       float ws = 1.f, bias = 0.f;
-      uint4 res[4];
+      uint32_t res[16];
       auto fetch = [&](int c) {
         const int n0 = nt * g.tn + 32 * c;
         const bool in = c < chunks && row0 < g.T && n0 + lane < g.N;
         if (FP8) ws = in ? __ldg(g.w_scale + static_cast<size_t>(n0 + lane) * g.w_scale_step) : 1.f;
         if (g.bias) bias = in ? load_typed(g.bias, g.bias_dt, n0 + lane) : 0.f;
-        if (!PROMOTE && g.res_vec && c < chunks && row0 < g.T && n0 + 32 <= g.N)
-          fetch_rows(res, static_cast<const unsigned short*>(g.residual), g.ldr, row0, g.T, n0, lane);
+        if (!PROMOTE && g.residual && c < chunks && row0 < g.T && n0 < g.N) fetch_residual<2, VEC>(g, res, row0, n0, lane);
       };
       auto finish = [&](float (&v)[32], int c) {
         const int n0 = nt * g.tn + 32 * c;
@@ -913,16 +964,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         __syncwarp();
         if (!in) return;
-        uint4 r[4];
-        if (!PROMOTE) {
+        uint32_t r[16];
+        if (PROMOTE) {
+          if (g.residual) fetch_residual<4, VEC>(g, r, row0, n0, lane);
+        } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) r[i] = res[i];
+          for (int i = 0; i < 16; ++i) r[i] = res[i];
         }
         fetch(c + 2);
         apply_act(v, g.act);
-        if (PROMOTE) tile_store_32(g, st, v, row0, n0, lane);
-        else if (g.out_dt == 0) tile_store_16<__nv_bfloat16>(g, st, v, r, row0, n0, lane);
-        else tile_store_16<__half>(g, st, v, r, row0, n0, lane);
+        if (PROMOTE) tile_store_32<VEC>(g, st, v, r, row0, n0, lane);
+        else if (g.out_dt == 0) tile_store_16<__nv_bfloat16, VEC>(g, st, v, r, row0, n0, lane);
+        else tile_store_16<__half, VEC>(g, st, v, r, row0, n0, lane);
       };
       fetch(half);
       auto release = [&](int acc) {
@@ -977,10 +1030,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   if constexpr (SPLIT) {
     cluster_sync_all();  // every partial tile is written
-    if (warp >= 4) {
+    if (warp >= 3) {
       int mt, nt;
       tile_coords(g, unit0, mt, nt);
-      split_rows(g, smem_u32(stages), ctarank, mt, nt, warp - 4, lane);
+      split_rows(g, smem_u32(stages), ctarank, mt, nt, warp - 3, lane);
     }
   }
   tc_fence_before();

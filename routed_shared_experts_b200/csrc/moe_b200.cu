@@ -445,6 +445,13 @@ moe_status_t make_linear_maps(CUtensorMap* m, CUtensorMap* tail, int dtype, cons
   return MOE_OK;
 }
 
+// The widest access (16, 4 or 2 bytes) that divides the address and the length
+// of every row.
+int row_unit(const void* base, size_t ld, int cols, int es) {
+  const size_t all = reinterpret_cast<uintptr_t>(base) | (ld * es) | (static_cast<size_t>(cols) * es);
+  return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : 2;
+}
+
 struct LinearCall {
   int dtype;
   const void *x, *w;
@@ -487,7 +494,7 @@ moe_status_t launch_linear_split(const LinearCall& c, int S, cudaStream_t s) {
   return MOE_OK;
 }
 
-template <bool FP8, bool PROMOTE, bool SPLIT>
+template <bool FP8, bool PROMOTE, bool SPLIT, bool VEC>
 moe_status_t launch_linear_tile(const LinearCall& c, int tn, int split, cudaStream_t s) {
   using L = moe::TileCfg;
   CUtensorMap tx, txt, tw, twt;
@@ -495,7 +502,7 @@ moe_status_t launch_linear_tile(const LinearCall& c, int tn, int split, cudaStre
   if (r != MOE_OK) return r;
   r = make_linear_maps(&tw, &twt, c.dtype, c.w, c.g.N, c.K, c.ldw, tn / 2);
   if (r != MOE_OK) return r;
-  auto kern = moe::k_linear_tile<FP8, PROMOTE, SPLIT>;
+  auto kern = moe::k_linear_tile<FP8, PROMOTE, SPLIT, VEC>;
   static std::atomic<int> attr_set[64];
   r = set_smem_attr(kern, 227 * 1024, attr_set);
   if (r != MOE_OK) return r;
@@ -506,9 +513,6 @@ moe_status_t launch_linear_tile(const LinearCall& c, int tn, int split, cudaStre
   const int64_t tiles = static_cast<int64_t>(g.n_tb) * g.n_nt;
   if (tiles > INT32_MAX / 16) return MOE_ERR_SHAPE;
   g.split = split;
-  const int os = float_size(g.out_dt);
-  g.out_vec = aligned16(g.out) && g.ldo * os % 16 == 0;
-  g.res_vec = g.residual && aligned16(g.residual) && g.ldr * os % 16 == 0;
   const int pairs = num_sms() / 2;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -533,9 +537,16 @@ struct LinearPlan {
 };
 
 template <bool FP8, bool PROMOTE>
-moe_status_t launch_linear_pairs(const LinearCall& c, const LinearPlan& p, cudaStream_t s) {
-  if (p.split > 1) return launch_linear_tile<FP8, PROMOTE, true>(c, p.tn, p.split, s);
-  return launch_linear_tile<FP8, PROMOTE, false>(c, p.tn, 1, s);
+moe_status_t launch_linear_pairs(LinearCall& c, const LinearPlan& p, cudaStream_t s) {
+  moe::LinearArgs& g = c.g;
+  const int os = float_size(g.out_dt);
+  g.out_unit = row_unit(g.out, g.ldo, g.N, os);
+  g.res_unit = g.residual ? row_unit(g.residual, g.ldr, g.N, os) : 16;
+  if (p.split > 1) return launch_linear_tile<FP8, PROMOTE, true, false>(c, p.tn, p.split, s);
+  // rows of whole 16-byte units take a kernel without the narrower accesses, which
+  // cost it registers (4096 x 7168 x 512: 35.7 against 41.3 us; an odd N: 49.7)
+  if (g.out_unit == 16 && g.res_unit == 16) return launch_linear_tile<FP8, PROMOTE, false, true>(c, p.tn, 1, s);
+  return launch_linear_tile<FP8, PROMOTE, false, false>(c, p.tn, 1, s);
 }
 
 // Clusters of the pair kernel (2 * split CTAs, one per SM) that run at one time.
@@ -546,7 +557,7 @@ int resident_clusters(int split) {
   std::atomic<int>& slot = cache[dev][split / 2];
   int n = slot.load();
   if (n) return n;
-  auto kern = moe::k_linear_tile<false, false, true>;
+  auto kern = moe::k_linear_tile<false, false, true, false>;
   static std::atomic<int> attr_set[64];
   if (set_smem_attr(kern, 227 * 1024, attr_set) != MOE_OK) return 1;
   cudaLaunchAttribute at[1];
@@ -618,7 +629,7 @@ LinearPlan plan_linear(int T, int N, int nk, bool f32_out) {
 }
 
 template <bool FP8>
-moe_status_t launch_linear(const LinearCall& c, cudaStream_t s) {
+moe_status_t launch_linear(LinearCall& c, cudaStream_t s) {
   const bool f32 = c.g.out_dt == MOE_DT_F32;
   const LinearPlan p = plan_linear(c.g.T, c.g.N, c.g.nk, f32);
   if (p.tn) return f32 ? launch_linear_pairs<FP8, true>(c, p, s) : launch_linear_pairs<FP8, false>(c, p, s);
