@@ -238,47 +238,56 @@ _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getC
 # kernels take a few microseconds: their checks are kept to attribute reads.
 
 
+def _refuse_device(first, others):
+    for t in others:
+        if t is not None and t.get_device() != first.get_device():
+            raise ValueError("tensors must live on one CUDA device")
+    raise ValueError(f"tensors on {first.device}: they must live on the current CUDA device")
+
+
 def _device(first, *others):
     """Index of the one device that every tensor lives on, the current one (the
     calls launch on its stream)."""
     dev = first.get_device()
     for t in others:
         if t is not None and t.get_device() != dev:
-            raise ValueError("tensors must live on one CUDA device")
+            _refuse_device(first, others)
     if dev < 0 or dev != _current_device():
-        raise ValueError(f"tensors on {first.device}: they must live on the current CUDA device")
+        _refuse_device(first, others)
     return dev
-
-
-def _raw_stream(stream, dev):
-    return _current_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _rows(t, name, rows, cols, types):
     """Row stride in elements of a [rows, cols] tensor whose rows are dense."""
+    if t.dtype in types and t.shape == (rows, cols):
+        ld, step = t.stride()
+        if step == 1 or cols == 1:
+            if rows < 2:
+                return -(-cols // 16) * 16  # the stride of a single row says nothing
+            if ld >= cols:
+                return ld
+        elif rows == 0:
+            return -(-cols // 16) * 16
+        raise ValueError(f"the rows of {name} must be contiguous and must not overlap")
+    _check_type(t, name, types)
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
+
+
+def _check_type(t, name, types):
     if t.dtype not in types:
         raise TypeError(f"{name} has type {t.dtype}")
-    if t.shape != (rows, cols):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
-    ld, step = t.stride()
-    if (step == 1 or cols == 1) and (rows == 1 or ld >= cols):
-        return ld if rows > 1 else -(-cols // 16) * 16  # the stride of a single row says nothing
-    if rows == 0:
-        return -(-cols // 16) * 16
-    raise ValueError(f"the rows of {name} must be contiguous and must not overlap")
 
 
 def _vec(t, name, n, types):
     """Address of a dense tensor of n elements (None: NULL)."""
     if t is None:
         return None
-    if t.dtype not in types:
-        raise TypeError(f"{name} has type {t.dtype}")
+    if t.dtype in types and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
+    _check_type(t, name, types)
     if t.numel() != n:
         raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def moe_linear(dtype, x, x_scale, w, w_scale, bias, act, residual, out, stream=None):
@@ -289,18 +298,26 @@ def moe_linear(dtype, x, x_scale, w, w_scale, bias, act, residual, out, stream=N
         raise MoEError("moe_linear", -2)
     T, K = x.shape
     N = w.shape[0]
+    out_type = out.dtype
     ldx = _rows(x, "x", T, K, types)
     ldw = _rows(w, "w", N, K, types)
     ldo = _rows(out, "out", T, N, _FLOAT_DT)
-    ldr = 0 if residual is None else _rows(residual, "residual", T, N, (out.dtype,))
     dev = _device(x, w, out, residual, bias, x_scale, w_scale)
-    ws_rows = 1 if w_scale is None else w_scale.numel()
-    _check("moe_linear", lib().moe_linear(
+    ldr, pr, pb, bias_dt, ws_rows = 0, None, None, MOE_DT_F32, 1
+    if residual is not None:
+        ldr = _rows(residual, "residual", T, N, (out_type,))
+        pr = residual.data_ptr()
+    if bias is not None:
+        pb = _vec(bias, "bias", N, _FLOAT_DT)
+        bias_dt = _FLOAT_DT[bias.dtype]
+    if w_scale is not None:
+        ws_rows = w_scale.numel()
+    status = (_LIB or lib()).moe_linear(
         dtype, x.data_ptr(), ldx, _vec(x_scale, "x_scale", T, _F32), w.data_ptr(), ldw,
-        _vec(w_scale, "w_scale", ws_rows, _F32), ws_rows, _vec(bias, "bias", N, _FLOAT_DT),
-        MOE_DT_F32 if bias is None else _FLOAT_DT[bias.dtype], act,
-        None if residual is None else residual.data_ptr(), ldr, out.data_ptr(), _FLOAT_DT[out.dtype], ldo, T, N, K,
-        _raw_stream(stream, dev)))
+        _vec(w_scale, "w_scale", ws_rows, _F32), ws_rows, pb, bias_dt, act, pr, ldr, out.data_ptr(),
+        _FLOAT_DT[out_type], ldo, T, N, K, _current_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        raise MoEError("moe_linear", status)
 
 
 def moe_route(logits, bias, expert_mask, num_valid, top_k, score, n_group, topk_group, group_score, renormalize,
@@ -309,13 +326,16 @@ def moe_route(logits, bias, expert_mask, num_valid, top_k, score, n_group, topk_
     any row stride."""
     T, E = logits.shape
     ld = _rows(logits, "logits", T, E, _FLOAT_DT)
-    dev = _device(logits, bias, expert_mask, num_valid, topk_ids, topk_weights)
-    _check("moe_route", lib().moe_route(
-        logits.data_ptr(), _FLOAT_DT[logits.dtype], ld, _vec(bias, "bias", E, _F32),
-        _vec(expert_mask, "expert_mask", E, _BYTES), _vec(num_valid, "num_valid", 1, _I32), T, E, top_k, score,
-        n_group, topk_group, group_score, renormalize, routed_scaling_factor,
-        _vec(topk_ids, "topk_ids", T * top_k, _I32), _vec(topk_weights, "topk_weights", T * top_k, _F32),
-        _raw_stream(stream, dev)))
+    dev = _device(logits, topk_ids, topk_weights, bias, expert_mask, num_valid)
+    n = T * top_k
+    status = (_LIB or lib()).moe_route(
+        logits.data_ptr(), _FLOAT_DT[logits.dtype], ld, bias if bias is None else _vec(bias, "bias", E, _F32),
+        expert_mask if expert_mask is None else _vec(expert_mask, "expert_mask", E, _BYTES),
+        num_valid if num_valid is None else _vec(num_valid, "num_valid", 1, _I32), T, E, top_k, score, n_group,
+        topk_group, group_score, renormalize, routed_scaling_factor, _vec(topk_ids, "topk_ids", n, _I32),
+        _vec(topk_weights, "topk_weights", n, _F32), _current_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        raise MoEError("moe_route", status)
 
 
 def moe_rmsnorm_quantize(quant, x, residual, gamma, eps, residual_out, y, codes, scale, stream=None):
@@ -326,10 +346,14 @@ def moe_rmsnorm_quantize(quant, x, residual, gamma, eps, residual_out, y, codes,
     xt = x.dtype
     same = (xt,)
     mx = quant == MOE_DT_MXFP8_E4M3
-    dev = _device(x, residual, gamma, residual_out, y, codes, scale)
-    _check("moe_rmsnorm_quantize", lib().moe_rmsnorm_quantize(
+    dev = _device(x, gamma, y, residual, residual_out, codes, scale)
+    status = (_LIB or lib()).moe_rmsnorm_quantize(
         _FLOAT_DT.get(xt, MOE_DT_F32), MOE_DT_NONE if quant is None else quant, _vec(x, "x", n, same),
-        _vec(residual, "residual", n, same), _vec(gamma, "gamma", H, (xt, torch.float32)),
-        _FLOAT_DT.get(gamma.dtype, MOE_DT_F32), eps, T, H, _vec(residual_out, "residual_out", n, same),
-        _vec(y, "y", n, same), _vec(codes, "codes", n, _CODES),
-        _vec(scale, "scale", n // 32 if mx else T, (torch.uint8,) if mx else _F32), _raw_stream(stream, dev)))
+        residual if residual is None else _vec(residual, "residual", n, same),
+        _vec(gamma, "gamma", H, (xt, torch.float32)), _FLOAT_DT.get(gamma.dtype, MOE_DT_F32), eps, T, H,
+        residual_out if residual_out is None else _vec(residual_out, "residual_out", n, same),
+        y if y is None else _vec(y, "y", n, same), codes if codes is None else _vec(codes, "codes", n, _CODES),
+        scale if scale is None else _vec(scale, "scale", n // 32 if mx else T, (torch.uint8,) if mx else _F32),
+        _current_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        raise MoEError("moe_rmsnorm_quantize", status)

@@ -237,6 +237,8 @@ __global__ void __launch_bounds__(kSplitThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  grid_dependents_launch();
+  grid_dependency_wait();
 
   if (warp == 0 || warp == 2) {
     if (elect_one()) {
@@ -776,6 +778,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   cluster_sync_all();  // both CTAs' barriers initialised before any remote use
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  grid_dependents_launch();
+  grid_dependency_wait();
 
   const int total = g.n_tb * g.n_nt;
   // SPLIT: one tile per cluster; else the pairs stride over the tiles

@@ -411,6 +411,33 @@ inline bool is_float_dt(int dtype) { return is_16bit(dtype) || dtype == MOE_DT_F
 inline int float_size(int dtype) { return dtype == MOE_DT_F32 ? 4 : 2; }
 inline bool aligned_to(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+// Launch that may start while the stream's previous kernel still drains (see
+// grid_dependency_wait): the kernel waits for it on the device. `early` = false
+// launches as usual (the kernel's wait then returns at once). `cluster`: CTAs
+// per cluster, or 0. Measured back to back in a graph: linear 5.8 -> 4.8 us (one
+// token, 2048 x 2048), 23.8 -> 23.1 us (fp8, 1024 x 5632 x 4096), norm 1.8 ->
+// 1.4 us and routing 3.8 -> 3.3 us (32 tokens).
+template <typename... P, typename... A>
+moe_status_t launch_early(void (*kern)(P...), unsigned grid, unsigned threads, size_t smem, unsigned cluster,
+                          bool early, cudaStream_t s, const A&... args) {
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = early;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster ? 2 : 1;
+  MOE_CK(cudaLaunchKernelEx(&cfg, kern, args...));
+  return MOE_OK;
+}
+
 // An operand of the linear product, `rows` rows of K elements, ld elements
 // apart: `m` as [atoms][rows][128 bytes] over the K atoms that K fills, read
 // kLinAtoms atoms x box_rows rows at a time, and `tail` as the plain matrix,
@@ -478,20 +505,7 @@ moe_status_t launch_linear_split(const LinearCall& c, int S, cudaStream_t s) {
   // one CTA per SM takes all of its shared memory for stages; more CTAs than
   // SMs share it two by two (N = 20000, K = 2048, one token: 16.7 against 21.2 us)
   const int n_stages = L::stages(ctas <= num_sms() ? 227 * 1024 : 113 * 1024);
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = static_cast<unsigned>(S);
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(moe::kSplitThreads);
-  cfg.dynamicSmemBytes = L::bytes(n_stages);
-  cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  MOE_CK(cudaLaunchKernelEx(&cfg, kern, tw, twt, tx, txt, g, S, n_stages));
-  return MOE_OK;
+  return launch_early(kern, ctas, moe::kSplitThreads, L::bytes(n_stages), S, true, s, tw, twt, tx, txt, g, S, n_stages);
 }
 
 template <bool FP8, bool PROMOTE, bool SPLIT, bool VEC>
@@ -514,20 +528,9 @@ moe_status_t launch_linear_tile(const LinearCall& c, int tn, int split, cudaStre
   if (tiles > INT32_MAX / 16) return MOE_ERR_SHAPE;
   g.split = split;
   const int pairs = num_sms() / 2;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = static_cast<unsigned>(SPLIT ? 2 * split : 2);
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(SPLIT ? 2 * tiles * split : 2 * (tiles < pairs ? tiles : pairs)));
-  cfg.blockDim = dim3(moe::kTileThreads);
-  cfg.dynamicSmemBytes = L::bytes(tn);
-  cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  MOE_CK(cudaLaunchKernelEx(&cfg, kern, tx, txt, tw, twt, g));
-  return MOE_OK;
+  const int ctas = static_cast<int>(SPLIT ? 2 * tiles * split : 2 * (tiles < pairs ? tiles : pairs));
+  return launch_early(kern, ctas, moe::kTileThreads, L::bytes(tn), SPLIT ? 2 * split : 2, true, s,
+                      tx, txt, tw, twt, g);
 }
 
 struct LinearPlan {
@@ -642,19 +645,16 @@ template <int VPL>
 moe_status_t launch_route(const moe::RouteArgs& a, bool softmax, cudaStream_t s) {
   const size_t smem = a.n_group > 1 ? moe::kRouteWarps * a.groups.words(a.n_group) * sizeof(float) : 0;
   const int blocks = (a.T + moe::kRouteWarps - 1) / moe::kRouteWarps;
-  if (softmax) moe::k_route<VPL, true><<<blocks, moe::kRouteWarps * 32, smem, s>>>(a);
-  else moe::k_route<VPL, false><<<blocks, moe::kRouteWarps * 32, smem, s>>>(a);
-  MOE_CK(cudaGetLastError());
-  return MOE_OK;
+  // a grid that fills the SMs gains nothing from a successor's waiting blocks (4096 tokens: 12.2 against 13.0 us)
+  return launch_early(softmax ? moe::k_route<VPL, true> : moe::k_route<VPL, false>, blocks, moe::kRouteWarps * 32, smem,
+                      0, blocks <= 2 * num_sms(), s, a);
 }
 
 template <typename TX, int Q, int TPR, int V>
 moe_status_t launch_rmsnorm(const moe::NormArgs& a, cudaStream_t s) {
   constexpr int threads = TPR > 256 ? TPR : 256;
   constexpr int rows = threads / TPR;
-  moe::k_rmsnorm<TX, Q, TPR, V><<<(a.T - 1) / rows + 1, threads, 0, s>>>(a);
-  MOE_CK(cudaGetLastError());
-  return MOE_OK;
+  return launch_early(moe::k_rmsnorm<TX, Q, TPR, V>, (a.T - 1) / rows + 1, threads, 0, 0, true, s, a);
 }
 
 // Threads per row and 16-byte chunks per thread, by the row's chunk count: one

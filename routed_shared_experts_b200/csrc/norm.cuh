@@ -95,6 +95,8 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) k_rmsnorm(const NormArg
   const uint4* x = reinterpret_cast<const uint4*>(static_cast<const TX*>(a.x) + base);
   const uint4* r = a.residual ? reinterpret_cast<const uint4*>(static_cast<const TX*>(a.residual) + base) : nullptr;
 
+  grid_dependents_launch();
+  grid_dependency_wait();
   uint4 xv[V], rv[V], gv[V];
 #pragma unroll
   for (int u = 0; u < V; ++u) {

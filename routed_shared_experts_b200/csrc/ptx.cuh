@@ -113,6 +113,15 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Programmatic launch of dependents: the first call lets the next kernel of the
+// stream start once every CTA of this one has started, the second waits until
+// the kernels before this one have completed and their writes are visible. A
+// kernel launched with launch_early() (host) calls both before its first access
+// to global memory, so only what comes before them - the launch itself, barriers,
+// TMEM - overlaps its predecessor.
+__device__ __forceinline__ void grid_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- TMA
 
 __device__ __forceinline__ uint64_t policy_evict_first() {

@@ -106,7 +106,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
   const int wib = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * kRouteWarps + wib;
+  grid_dependents_launch();
   if (t >= a.T) return;
+  grid_dependency_wait();
   const float NEG_INF = __int_as_float(0xff800000);
   const size_t row = static_cast<size_t>(t) * a.ld;
 
