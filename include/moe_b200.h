@@ -458,8 +458,8 @@ moe_status_t shared_expert_gate_dot(int dtype, const void* x, const void* w, int
  *              per output) or 1 (one per matrix): FP8 only, NULL otherwise.
  *   bias       [N] of bias_dtype (BF16, FP16, F32), or NULL.
  *   act        MOE_ACT_*, evaluated in fp32 with the fast exponential
- *              (relative error near 2^-21); NaN and infinities follow the
- *              formula.
+ *              (relative error near 2^-21; GELU's error function adds
+ *              2^-24 |v|); NaN and infinities follow the formula.
  *   residual   [T,N] of out_dtype, rows ldr apart, or NULL. It may be out
  *              itself (same address and stride); any other overlap of out
  *              with an operand is undefined.
@@ -467,8 +467,8 @@ moe_status_t shared_expert_gate_dot(int dtype, const void* x, const void* w, int
  *              between the rows is written.
  * No workspace; results do not depend on the launch (a K split is added in a
  * fixed order), but sums of different T, N or K may be ordered differently.
- * Checks: T >= 0 (T == 0: nothing is launched), N, K >= 1, ldx, ldw >= K,
- * ldo, ldr >= N; x and w 16-byte aligned with row strides of a multiple of 16
+ * Checks: T >= 0 (T == 0: nothing is launched), N, K >= 1, none above 2^30,
+ * ldx, ldw >= K, ldo, ldr >= N, none above 2^36; x and w 16-byte aligned with row strides of a multiple of 16
  * bytes (MOE_ERR_ALIGNMENT), out, residual, bias and the scales aligned to
  * their own type. Asynchronous on `stream`, a stream of the current device. */
 moe_status_t moe_linear(int dtype, const void* x, int64_t ldx, const float* x_scale, const void* w,

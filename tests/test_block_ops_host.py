@@ -42,7 +42,8 @@ def _linear(lib, **kw):
     (dict(dt=capi.MOE_DT_FP8_E4M3, xs=P, ws=P, ldx=72), ALIGN), (dict(o=P + 1), ALIGN), (dict(r=P + 1, ldr=32), ALIGN),
     (dict(odt=capi.MOE_DT_F32, o=P + 2), ALIGN), (dict(b=P + 2), ALIGN),
     (dict(dt=capi.MOE_DT_FP8_E4M3, xs=P + 1, ws=P), ALIGN), (dict(dt=capi.MOE_DT_FP8_E4M3, xs=P, ws=P + 2), ALIGN),
-    (dict(ldx=1 << 37), SHAPE), (dict(ldo=(1 << 36) + 1), SHAPE), (dict(r=P, ldr=1 << 40), SHAPE),
+    (dict(T=(1 << 30) + 1), SHAPE), (dict(N=(1 << 30) + 1, ldo=1 << 31), SHAPE),
+    (dict(K=(1 << 30) + 8, ldx=1 << 31, ldw=1 << 31), SHAPE), (dict(ldx=1 << 37), SHAPE), (dict(ldo=(1 << 36) + 1), SHAPE), (dict(r=P, ldr=1 << 40), SHAPE),
     (dict(T=0), 0), (dict(T=0, x=None, o=None), 0),
 ])
 def test_linear_refusals(lib, kw, want):
