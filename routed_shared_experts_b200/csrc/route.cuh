@@ -214,37 +214,49 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
     }
   }
 
-  // k rounds; lane j keeps the j-th pick. best / bi: this lane's best key and
-  // the lowest slot that holds it.
-  uint32_t best = 0;
-  int bi = 0;
+  // k rounds; lane j keeps the j-th pick. k1 / i1: this lane's best key and the
+  // lowest slot that holds it. With eight slots or more also the next, k2 / i2:
+  // such a lane looks through its slots again only when both are gone, which few
+  // rows come to (4096 x 256: 11.3 against 12.2 us; 32 x 128, four slots, 3.5
+  // against 3.4).
+  constexpr bool kTwo = VPL >= 8;
+  uint32_t k1, k2, taken = 0;
+  int i1, i2;
+  auto scan = [&]() {
+    k1 = k2 = 0;
+    i1 = i2 = 0;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i)
-    if (key[i] > best) {
-      best = key[i];
-      bi = i;
+    for (int i = 0; i < VPL; ++i) {
+      const uint32_t v = (taken >> i) & 1u ? 0u : key[i];
+      if (v > k1) {
+        k2 = k1, i2 = i1;
+        k1 = v, i1 = i;
+      } else if (kTwo && v > k2) {
+        k2 = v, i2 = i;
+      }
     }
-  __syncwarp();  // p_sm
+  };
+  scan();
+  bool second = kTwo;  // k2 / i2 hold the lane's next
+  __syncwarp();        // p_sm
   int sel = 0;
   bool live = false;
   for (int j = 0; j < a.k; ++j) {
-    const uint32_t m = __reduce_max_sync(0xffffffffu, best);
-    const unsigned e = __reduce_min_sync(0xffffffffu, best == m ? static_cast<unsigned>(lane + 32 * bi) : 0xffffffffu);
+    const uint32_t m = __reduce_max_sync(0xffffffffu, k1);
+    const unsigned e = __reduce_min_sync(0xffffffffu, k1 == m ? static_cast<unsigned>(lane + 32 * i1) : 0xffffffffu);
     if (lane == j) {
       sel = static_cast<int>(e);
       live = m > kDeadKey;
     }
-    if (lane == static_cast<int>(e & 31u)) {  // this lane's next best
-      const int gone = static_cast<int>(e >> 5);
-      best = 0;
-      bi = 0;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        if (i == gone) key[i] = 0;
-        if (key[i] > best) {
-          best = key[i];
-          bi = i;
-        }
+    if (lane == static_cast<int>(e & 31u)) {
+      taken |= 1u << i1;
+      if (second) {
+        k1 = k2;
+        i1 = i2;
+        second = false;
+      } else {
+        scan();
+        second = kTwo;
       }
     }
   }
