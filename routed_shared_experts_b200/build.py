@@ -2,8 +2,8 @@
 
     python -m routed_shared_experts_b200.build [--force] [--ptxas-info]
 
-The library is one translation unit (``csrc/moe_b200.cu`` includes the kernel
-headers). The CUDA runtime is linked statically, so loading the library needs
+The library is one translation unit (``csrc/block_ops.cu`` includes
+``csrc/moe_b200.cu``, and both the kernel headers). The CUDA runtime is linked statically, so loading the library needs
 no GPU and no libcuda; the driver API entry point for TMA descriptors is looked
 up at run time.
 """
@@ -51,7 +51,7 @@ def build(force: bool = False, ptxas_info: bool = False, out: str = LIB_PATH) ->
     if not force and out == LIB_PATH and up_to_date():
         return out
     cmd = [_nvcc(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC,-O3", "-shared",
-           "-cudart", "static", "-I", INCLUDE, "-I", CSRC, "-o", out, os.path.join(CSRC, "moe_b200.cu")]
+           "-cudart", "static", "-I", INCLUDE, "-I", CSRC, "-o", out, os.path.join(CSRC, "block_ops.cu")]
     if ptxas_info:
         cmd[1:1] = ["-Xptxas", "-v"]
     res = subprocess.run(cmd, capture_output=True, text=True)

@@ -30,6 +30,7 @@
 
 #include "gemm.cuh"
 #include "norm.cuh"
+#include "ptx_ext.cuh"
 #include "router.cuh"
 
 namespace moe {

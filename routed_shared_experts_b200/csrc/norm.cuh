@@ -14,6 +14,7 @@
 // to a block of 256 threads so that a block always has 256 threads' loads in
 // flight.
 #pragma once
+#include "ptx_ext.cuh"
 #include "quant.cuh"
 #include "router.cuh"
 

@@ -26,6 +26,7 @@
 // reciprocal by Newton's iteration, which needs no special cases for a divisor
 // in [1, 512]. The scores of a softmax stay in shared memory for the weights.
 #pragma once
+#include "ptx_ext.cuh"
 #include "router.cuh"
 
 namespace moe {

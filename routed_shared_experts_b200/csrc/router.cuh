@@ -6,7 +6,7 @@
 #pragma once
 #include <cooperative_groups.h>
 
-#include "ptx.cuh"
+#include "ptx_ext.cuh"
 
 namespace moe {
 

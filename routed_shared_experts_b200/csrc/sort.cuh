@@ -6,7 +6,7 @@
 // touches the output (the stage-2 epilogue writes every output row).
 // ROCm/aiter PR 6106, "Technical Details": GEMM rows follow this gather index.
 #pragma once
-#include "ptx.cuh"
+#include "ptx_ext.cuh"
 
 namespace moe {
 
