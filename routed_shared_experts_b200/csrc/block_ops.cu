@@ -104,13 +104,11 @@ moe_status_t launch_linear_split(const LinearCall& c, int S, cudaStream_t s) {
   static std::atomic<int> attr_set[64];
   r = set_smem_attr(kern, 227 * 1024, attr_set);
   if (r != MOE_OK) return r;
-  moe::LinearArgs g = c.g;
-  g.n_tb = 1;
-  const int ctas = (g.N - 1) / moe::kTileM * S + S;
+  const int ctas = (c.g.N - 1) / moe::kTileM * S + S;
   // one CTA per SM takes all of its shared memory for stages; more CTAs than
   // SMs share it two by two (N = 20000, K = 2048, one token: 16.7 against 21.2 us)
   const int n_stages = L::stages(ctas <= num_sms() ? 227 * 1024 : 113 * 1024);
-  return launch_early(kern, ctas, moe::kSplitThreads, L::bytes(n_stages), S, true, s, tw, twt, tx, txt, g, S, n_stages);
+  return launch_early(kern, ctas, moe::kSplitThreads, L::bytes(n_stages), S, true, s, tw, twt, tx, txt, c.g, S, n_stages);
 }
 
 template <bool FP8, bool PROMOTE, bool SPLIT, bool VEC>

@@ -24,7 +24,10 @@
 // order in which CTAs finish.
 // What bounds it: with few tokens the weights' stream from HBM, N * K * size
 // bytes, which needs all SMs pulling at once; the K split is what supplies them
-// when N / 128 tiles are fewer than the SMs.
+// when N / 128 tiles are fewer than the SMs (32 tokens, 7168 x 7168 with
+// residual: 19.9 us, 5.2 TB/s, 81 % of the measured copy rate; the library's
+// product alone 26.0). Below about 10 MB of weights it is bound by latency: 4.7
+// us for one token against 2048 x 2048.
 #pragma once
 #include <type_traits>
 
@@ -55,7 +58,7 @@ struct LinearArgs {
   void* out;  // rows ldo apart
   size_t ldo;
   int out_dt;  // MOE_DT_BF16, MOE_DT_FP16 or MOE_DT_F32
-  int n_tb;    // token blocks (k_linear_split) or 256-token tiles (k_linear_tile)
+  int n_tb;    // k_linear_tile: 256-token tiles
   int tn, n_nt;  // k_linear_tile: outputs per tile (a multiple of 32, at most 256), tiles along N
   int split;     // k_linear_tile with SPLIT: pairs along K
   int out_unit, res_unit;  // k_linear_tile: bytes that divide every row's address and length: 16, 4 or 2
@@ -211,7 +214,7 @@ struct SplitOut {
   // `part`: this thread's output of column 0), this CTA's own first, so that the
   // peers' reads spread.
   template <int C>
-  __device__ __forceinline__ void join(uint32_t part, int rank, int S, int c0, int c_hi, int t_base,
+  __device__ __forceinline__ void join(uint32_t part, int rank, int S, int c0, int c_hi,
                                        const float (&r)[B]) const {
     float v[C];
 #pragma unroll
@@ -223,7 +226,7 @@ struct SplitOut {
       for (int i = 0; i < C; ++i)
         if (c0 + i < c_hi) v[i] += ld_shared_cluster_f32(peer + static_cast<uint32_t>((c0 + i) * kTileM * 4));
     }
-    finish(v, r, t_base + c0, t_base + c_hi);
+    finish(v, r, c0, c_hi);
   }
 };
 
@@ -247,9 +250,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rank = static_cast<int>(blockIdx.x) % S;  // clusters are S consecutive CTAs
-  const int tile = static_cast<int>(blockIdx.x) / S;
-  const int nt = tile / g.n_tb;
-  const int t_base = (tile - nt * g.n_tb) * BN;
+  const int nt = static_cast<int>(blockIdx.x) / S;
   const int ns = (g.nk + kLinAtoms - 1) / kLinAtoms;  // stages along K; this CTA's are s0 .. s1 - 1
   const int s0 = static_cast<int>(static_cast<long long>(ns) * rank / S);
   const int s1 = static_cast<int>(static_cast<long long>(ns) * (rank + 1) / S);
@@ -280,9 +281,8 @@ __global__ void __launch_bounds__(kSplitThreads)
       const bool is_w = warp == 0;
       const CUtensorMap* tm = is_w ? &tmW : &tmX;
       const CUtensorMap* tail = is_w ? &tmWt : &tmXt;
-      // weights pass once through L2 when one token block reads them
-      const uint64_t pol = is_w && g.n_tb == 1 ? policy_evict_first() : policy_evict_last();
-      const int row0 = is_w ? nt * kTileM : t_base;
+      const uint64_t pol = is_w ? policy_evict_first() : policy_evict_last();  // the weights pass once
+      const int row0 = is_w ? nt * kTileM : 0;
       const int atom_bytes = is_w ? L::kAtomW : L::kAtomX;
       const int off = is_w ? 0 : L::kAtomW * kLinAtoms;
       int stage = 0;
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   const int q = warp & 3;  // TMEM lane quarter of an epilogue warp
   const int rowi = 32 * q + lane;
   const int n = nt * kTileM + rowi;
-  const int nv = min(BN, g.T - t_base);  // tokens of this block
+  const int nv = min(BN, g.T);  // tokens
   // S > 1: this CTA finishes columns c_lo .. c_hi - 1
   const int c_lo = nv * rank / S, c_hi = nv * (rank + 1) / S;
   constexpr int B = BN == 16 ? 8 : 16;
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kSplitThreads)
       if (g.x_scale) o.ws = __ldg(g.w_scale + static_cast<size_t>(n) * g.w_scale_step);
       if (g.bias) o.bias = load_typed(g.bias, g.bias_dt, n);
     }
-    o.residual_of(res, t_base + c_lo, t_base + c_hi);
+    o.residual_of(res, c_lo, c_hi);
     ok = mbar_wait(done, 0, abort_flag);
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
@@ -379,12 +379,12 @@ __global__ void __launch_bounds__(kSplitThreads)
         tmem_wait_ld();
 #pragma unroll
         for (int h = 0; h < 16 / B; ++h) {
-          const int t0 = t_base + c0 + B * h;
+          const int t0 = c0 + B * h;
           float u[B];
 #pragma unroll
           for (int i = 0; i < B; ++i) u[i] = v[B * h + i];
-          if (c0 + h > 0) o.residual_of(res, t0, t_base + nv);
-          o.finish(u, res, t0, t_base + nv);
+          if (c0 + h > 0) o.residual_of(res, t0, nv);
+          o.finish(u, res, t0, nv);
         }
       }
     }
@@ -404,12 +404,12 @@ __global__ void __launch_bounds__(kSplitThreads)
     if (warp >= 3) {
       const uint32_t part0 = smem_u32(part) + 4u * static_cast<uint32_t>(rowi);
       for (int c0 = c_lo; c0 < c_hi;) {
-        if (c0 > c_lo) o.residual_of(res, t_base + c0, t_base + c_hi);
+        if (c0 > c_lo) o.residual_of(res, c0, c_hi);
         if (B == 8 || c_hi - c0 <= 8) {
-          o.template join<8>(part0, rank, S, c0, c_hi, t_base, res);
+          o.template join<8>(part0, rank, S, c0, c_hi, res);
           c0 += 8;
         } else {
-          o.template join<B>(part0, rank, S, c0, c_hi, t_base, res);
+          o.template join<B>(part0, rank, S, c0, c_hi, res);
           c0 += B;
         }
       }
@@ -428,13 +428,21 @@ __global__ void __launch_bounds__(kSplitThreads)
 //
 // k_linear_tile: a 2-CTA cluster per tile of 256 tokens (M, 128 in each CTA)
 // x tn outputs (N, tn / 2 weight rows in each CTA), persistent over the tiles.
-// Warp 0 loads (each CTA its half of both operands), rank 0's warp 1 issues
-// the pair's MMAs, and eight epilogue warps per CTA empty one TMEM accumulator
-// while the MMAs fill the other. tn is chosen by the host so that the tiles
-// fill whole waves of pairs. Each epilogue warp owns 32 token rows and turns
-// its columns, 32 at a time, through 2 KB of shared memory, so that residual
-// reads and result writes are whole 64-byte row segments and no barrier between
-// warps is needed.
+// Warps 0 and 2 load (tokens and weights, each CTA its half of both), rank 0's
+// warp 1 issues the pair's MMAs, and eight epilogue warps per CTA empty one TMEM
+// accumulator while the MMAs fill the other. tn is chosen by the host so that the
+// tiles fill whole waves of pairs. Each epilogue warp owns 32 token rows and
+// turns its columns, 32 at a time, through 2 KB of shared memory, so that
+// residual reads and result writes are whole 64-byte row segments and no barrier
+// between warps is needed.
+//
+// What bounds it: at tn = 256 the MMAs (a stage of two atoms takes 1023 of the
+// ideal 1024 clocks), under the 1 kW power cap at T = 4096, N = K = 7168 (294 us
+// with residual, the library's product alone 304; 1.43 PFLOP/s against 1.38
+// sustained measured). Narrow tiles wait for their copies, whose round trip of
+// about 1.45 us the stages that fit have to cover: hence as many as fit. Small
+// shapes are bound by what a launch, the first copy and the last tile's epilogue
+// take, 5 to 7 us.
 //
 // SPLIT: the K axis of a tile is divided over the `split` pairs of one cluster,
 // for shapes whose tiles are fewer than the pairs of SMs. As in k_linear_split
@@ -653,8 +661,8 @@ __device__ __forceinline__ void tile_coords(const LinearArgs& g, int tile, int& 
   mt = band * kBand + (i - nt * rows);
 }
 
-// SPLIT: rows [lo, hi) of this CTA's 128 from the S partial tiles, one warp per
-// row, four columns per lane. A partial tile is [128][tn] fp32 in 16-byte units,
+// SPLIT: rows [lo, hi) of this CTA's 128 from the S partial tiles, a warp per two
+// rows, four columns per lane. A partial tile is [128][tn] fp32 in 16-byte units,
 // unit u of row r at u ^ (r & 7).
 __device__ __forceinline__ int part_unit(int r, int u, int tn) { return r * (tn / 4) + (u ^ (r & 7)); }
 

