@@ -92,6 +92,8 @@ CASES = [
     (configs.MXFP8_PREFILL, dict(T=300, H=512, E=8, top_k=2, I=256, Is=256, n_group=4, topk_group=2), MoELayer, False),
     (configs.MXFP8_PREFILL, dict(T=1, H=512, E=8, top_k=2, I=256, Is=256, n_group=4, topk_group=2, block_m=16),
      FusedSharedMoELayer, False),
+    # one expert per token: stage 2 writes each row without its workspace
+    (configs.DECODE_BF16, dict(T=48, H=512, E=16, top_k=1, I=128, Is=128), MoELayer, False),
 ]
 
 
@@ -123,7 +125,7 @@ def test_block(cuda_lib, case, general):
     assert torch.count_nonzero(block.layer.acc_ws).item() == 0
 
 
-@pytest.mark.parametrize("case", [0, 1, 2, 3])
+@pytest.mark.parametrize("case", [0, 1, 2, 3, 5])
 def test_block_padded_batches_from_one_graph(cuda_lib, case):
     """One captured graph serves batches of every length: the rows behind
     num_valid take no expert, keep what the output held, and leave the

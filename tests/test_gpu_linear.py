@@ -245,7 +245,7 @@ def test_linear_wrapper_refusals(cuda_lib):
         capi.moe_linear(bf, x, None, w, None, None, 17, None, out)
 
 
-@pytest.mark.parametrize("T,N,K", [(8, 512, 2048), (700, 1100, 512)])
+@pytest.mark.parametrize("T,N,K", [(8, 512, 2048), (40, 4000, 512), (200, 512, 4096), (700, 1100, 512)])
 def test_linear_repeatable_and_concurrent(cuda_lib, T, N, K):
     """The same bits every time, two calls at once on two streams included, and
     from a captured graph replayed on new inputs."""
@@ -273,3 +273,21 @@ def test_linear_repeatable_and_concurrent(cuda_lib, T, N, K):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(o, want[i])
+
+
+@pytest.mark.parametrize("T,gap", [(64, 70_000_000), (120, 40_000_000), (3000, 1_600_000)])
+def test_linear_offsets_past_32_bits(cuda_lib, T, gap):
+    """Rows far apart: operands, residual and result reach past 2^32 elements."""
+    N, K = 333, 136
+    big = torch.empty((T - 1) * gap + 4096, dtype=torch.bfloat16, device="cuda")
+    view = lambda cols, at: torch.as_strided(big, (T, cols), (gap, 1), at)  # noqa: E731
+    x, r, out = view(K, 0), view(N, 512), view(N, 1024)
+    g = torch.Generator().manual_seed(T)
+    x.copy_(torch.randint(-3, 4, (T, K), generator=g).to(torch.bfloat16))
+    r.copy_(torch.randint(-9, 10, (T, N), generator=g).to(torch.bfloat16))
+    w = torch.randint(-3, 4, (N, K), generator=g).to(torch.bfloat16).cuda()
+    capi.moe_linear(capi.MOE_DT_BF16, x, None, w, None, None, 0, r, out)
+    torch.cuda.synchronize()
+    assert capi.device_error() == 0
+    ref = (x.double() @ w.double().t() + r.double()).to(torch.bfloat16)
+    assert torch.equal(out, ref)

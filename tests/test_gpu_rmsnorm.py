@@ -202,3 +202,22 @@ def test_norm_no_rows_graph_and_refusals(cuda_lib):
         capi.moe_rmsnorm_quantize(None, x.float(), None, g.float(), 1e-6, None, y.float(), None, None)
     with pytest.raises(capi.MoEError):
         capi.moe_rmsnorm_quantize(None, x, None, g, 0.0, None, y, None, None)
+
+
+def test_norm_offsets_past_32_bits(cuda_lib):
+    """In place over more than 2^32 values: the last rows like the first."""
+    T, H = 530_000, 8192
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator().manual_seed(1)
+    rows = torch.randn((4, H), generator=g).bfloat16().cuda()
+    at = [0, 1, T - 2, T - 1]
+    for i, t in enumerate(at):
+        x[t] = rows[i]
+    gamma = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    want = torch.empty_like(rows)
+    capi.moe_rmsnorm_quantize(None, rows, None, gamma, 1e-6, None, want, None, None)
+    capi.moe_rmsnorm_quantize(None, x, None, gamma, 1e-6, None, x, None, None)
+    torch.cuda.synchronize()
+    for i, t in enumerate(at):
+        assert torch.equal(x[t], want[i])
+    assert torch.count_nonzero(x[2:T - 2][::997]).item() == 0

@@ -151,6 +151,22 @@ def test_route_strided_logits(cuda_lib, dt):
     _check(wide[::2, 1:65], None, None, 4, "sigmoid")
 
 
+def test_route_offsets_past_32_bits(cuda_lib):
+    """Logit rows far apart, the last one past 2^32 elements."""
+    T, E, gap = 3000, 40, 1_600_000
+    big = torch.empty((T - 1) * gap + E, dtype=torch.bfloat16, device="cuda")
+    logits = torch.as_strided(big, (T, E), (gap, 1))
+    logits.copy_(torch.randn((T, E), generator=torch.Generator().manual_seed(3)).bfloat16())
+    out = []
+    for l in (logits, logits.contiguous()):
+        ids = torch.empty((T, 4), dtype=torch.int32, device="cuda")
+        w = torch.empty((T, 4), device="cuda")
+        capi.moe_route(l, None, None, None, 4, capi.MOE_SCORE_SIGMOID, 4, 2, capi.MOE_GROUP_TOP2, True, 1.0, ids, w)
+        out.append((ids, w))
+    torch.cuda.synchronize()
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+
+
 def test_route_softmax_agrees_with_the_plain_top_k(cuda_lib):
     """No bias, no groups: the same experts and weights as moe_router_topk."""
     g = torch.Generator().manual_seed(2)
