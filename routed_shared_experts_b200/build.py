@@ -1,4 +1,5 @@
-"""Build ``libmoe_b200.so`` (sm_100a) in-tree with nvcc.
+"""Build ``libmoe_b200.so`` (sm_100a) in-tree with nvcc, and with gcc the Python
+binding ``_binding.so`` of its small operators.
 
     python -m routed_shared_experts_b200.build [--force] [--ptxas-info]
 
@@ -14,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libmoe_b200.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
+BINDING_PATH = os.path.join(PKG, "_binding.so")  # csrc/binding.c, the Python fast path of the small operators
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -47,7 +50,22 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(s) <= t for s in _sources())
 
 
+def build_binding(force: bool = False) -> str:
+    src = os.path.join(CSRC, "binding.c")
+    if not force and os.path.exists(BINDING_PATH) and os.path.getmtime(src) <= os.path.getmtime(BINDING_PATH):
+        return BINDING_PATH
+    cmd = [shutil.which("gcc") or "cc", "-O2", "-fPIC", "-shared", "-Wall", "-I",
+           sysconfig.get_paths()["include"], "-o", BINDING_PATH, src]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError(f"gcc failed ({res.returncode})")
+    return BINDING_PATH
+
+
 def build(force: bool = False, ptxas_info: bool = False, out: str = LIB_PATH) -> str:
+    if out == LIB_PATH:
+        build_binding(force)
     if not force and out == LIB_PATH and up_to_date():
         return out
     cmd = [_nvcc(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xcompiler", "-fPIC,-O3", "-shared",

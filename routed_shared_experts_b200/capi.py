@@ -84,8 +84,25 @@ def lib() -> ctypes.CDLL:
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args
+        _load_binding(handle)
         _LIB = handle
     return _LIB
+
+
+_BINDING = None  # csrc/binding.c: well-formed calls of the small operators without ctypes
+
+
+def _load_binding(handle):
+    global _BINDING
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise RuntimeError("the Python binding is missing: build it with python -m routed_shared_experts_b200.build") from e
+    address = lambda name: ctypes.cast(getattr(handle, name), ctypes.c_void_p).value  # noqa: E731
+    _binding.init((address("moe_linear"), address("moe_route"), address("moe_rmsnorm_quantize")),
+                  (torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn, torch.uint8, torch.bool,
+                   torch.int32), torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    _BINDING = _binding
 
 
 def _ptr(t):
@@ -234,8 +251,15 @@ _CODES = (torch.uint8, torch.float8_e4m3fn)
 
 _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
-# The wrappers below are called once per operator of a decode step, whose
-# kernels take a few microseconds: their checks are kept to attribute reads.
+# The wrappers below are called once per operator of a decode step, whose kernels
+# take a few microseconds. The binding makes a well-formed call (None: it is not
+# one); the checks here name what is wrong with the others, and make the calls
+# that the binding leaves alone (no rows).
+
+
+def _binding():
+    lib()
+    return _BINDING
 
 
 def _refuse_device(first, others):
@@ -293,6 +317,11 @@ def _vec(t, name, n, types):
 def moe_linear(dtype, x, x_scale, w, w_scale, bias, act, residual, out, stream=None):
     """out = act((x . w^T) * x_scale * w_scale + bias) + residual; x [T,K], w
     [N,K], residual and out [T,N] may be views with any row stride."""
+    status = (_BINDING or _binding()).linear(dtype, x, x_scale, w, w_scale, bias, act, residual, out, stream)
+    if status is not None:
+        if status:
+            raise MoEError("moe_linear", status)
+        return
     types = _OPERAND_DT.get(dtype)
     if types is None:
         raise MoEError("moe_linear", -2)
@@ -324,6 +353,13 @@ def moe_route(logits, bias, expert_mask, num_valid, top_k, score, n_group, topk_
               routed_scaling_factor, topk_ids, topk_weights, stream=None):
     """Routing from softmax or sigmoid scores; logits [T,E] may be a view with
     any row stride."""
+    status = (_BINDING or _binding()).route(logits, bias, expert_mask, num_valid, top_k, score, n_group, topk_group,
+                                            group_score, renormalize, routed_scaling_factor, topk_ids, topk_weights,
+                                            stream)
+    if status is not None:
+        if status:
+            raise MoEError("moe_route", status)
+        return
     T, E = logits.shape
     ld = _rows(logits, "logits", T, E, _FLOAT_DT)
     dev = _device(logits, topk_ids, topk_weights, bias, expert_mask, num_valid)
@@ -341,6 +377,12 @@ def moe_route(logits, bias, expert_mask, num_valid, top_k, score, n_group, topk_
 def moe_rmsnorm_quantize(quant, x, residual, gamma, eps, residual_out, y, codes, scale, stream=None):
     """z = x + residual -> residual_out; RMS norm of z -> y and / or codes with
     scale. ``quant``: MOE_DT_FP8_E4M3, MOE_DT_MXFP8_E4M3, or None."""
+    status = (_BINDING or _binding()).rmsnorm_quantize(MOE_DT_NONE if quant is None else quant, x, residual, gamma, eps,
+                                                       residual_out, y, codes, scale, stream)
+    if status is not None:
+        if status:
+            raise MoEError("moe_rmsnorm_quantize", status)
+        return
     T, H = x.shape
     n = T * H
     xt = x.dtype

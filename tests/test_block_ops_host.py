@@ -118,3 +118,22 @@ def test_constants_match_the_header():
         assert int(val["MOE_ACT_" + name.upper()]) == v
     for name in ("MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "MOE_GROUP_TOP2", "MOE_GROUP_MAX"):
         assert int(val[name]) == getattr(capi, name)
+
+
+def test_binding_leaves_malformed_calls_alone(lib):
+    """The binding answers None, without an exception and without keeping a
+    reference, to whatever is not a well-formed call."""
+    import sys
+    b = capi._binding()
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    objs = [x, None, 3, "text", object(), (1, 2)]
+    counts = [sys.getrefcount(v) for v in objs]
+    for _ in range(50):
+        for o in objs:
+            assert b.linear(0, o, None, x, None, None, 0, None, o, None) is None
+            assert b.route(o, None, None, None, 2, 0, 1, 1, 0, True, 1.0, o, o, None) is None
+            assert b.rmsnorm_quantize(-1, o, None, x, 1e-6, None, o, None, None, None) is None
+        assert b.linear() is None and b.route(1) is None and b.rmsnorm_quantize(*range(10)) is None
+        assert b.linear("bf16", x, None, x, None, None, "relu", None, x, None) is None
+    del o  # the loop's own reference to the last one
+    assert [sys.getrefcount(v) for v in objs] == counts

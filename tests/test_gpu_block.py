@@ -187,3 +187,48 @@ def test_block_refusals(cuda_lib):
         MoELayer(cfg, inp, router_gemm=True, routing=Routing())
     with pytest.raises(ValueError):
         MoEBlock(MoELayer(cfg, inp, router_gemm=True), {}, None, None)
+
+
+class _NoFastPath:
+    """A binding that leaves every call to the checked path."""
+
+    def __getattr__(self, name):
+        return lambda *a: None
+
+
+def test_both_paths_of_the_wrappers_agree(cuda_lib, monkeypatch):
+    """The binding and the checked path make the same calls: same bits, on
+    operands of every kind, and the binding keeps no references."""
+    import sys
+    g = torch.Generator().manual_seed(5)
+    wide = torch.randn((9, 200), generator=g).bfloat16().cuda()
+    x, w = wide[:, 8:136], torch.randn((24, 128), generator=g).bfloat16().cuda()
+    f8 = [torch.randint(0, 120, s, generator=g, dtype=torch.uint8).cuda() for s in ((9, 128), (24, 128))]
+    xs, ws, bias = torch.rand(9, generator=g).cuda(), torch.rand(1, generator=g).cuda(), torch.rand(24, generator=g).cuda()
+    r = torch.randn((9, 24), generator=g).bfloat16().cuda()
+    mask, nv = torch.tensor([1, 0] * 12, dtype=torch.bool).cuda(), torch.tensor([7], dtype=torch.int32).cuda()
+    gamma = torch.rand(128, generator=g).cuda()
+    side = torch.cuda.Stream()
+
+    def run():
+        out = [torch.empty((9, 24), dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+        capi.moe_linear(capi.MOE_DT_BF16, x, None, w, None, bias, 2, r, out[0])
+        capi.moe_linear(capi.MOE_DT_FP8_E4M3, f8[0].view(torch.float8_e4m3fn), xs, f8[1], ws, None, 0, None, out[1])
+        capi.moe_linear(capi.MOE_DT_BF16, x[:1], None, w, None, None, 0, None, out[2][:1])
+        ids, wt = torch.empty((9, 3), dtype=torch.int32, device="cuda"), torch.empty((9, 3), device="cuda")
+        side.wait_stream(torch.cuda.current_stream())
+        capi.moe_route(out[0], bias, mask, nv, 3, 1, 4, 3, 1, False, 2.5, ids, wt, side)
+        y, c = torch.empty((9, 128), dtype=torch.bfloat16, device="cuda"), torch.empty((9, 128), dtype=torch.uint8, device="cuda")
+        s = torch.empty((9, 4), dtype=torch.uint8, device="cuda")
+        capi.moe_rmsnorm_quantize(capi.MOE_DT_MXFP8_E4M3, x.contiguous(), None, gamma, 1e-5, None, y, c, s)
+        torch.cuda.synchronize()
+        return [out[0], out[1], out[2][:1], ids, wt, y, c, s]
+
+    fast = run()
+    counts = [sys.getrefcount(o) for o in (x, w, bias, r, mask, nv, gamma, side, torch.bfloat16, torch.uint8)]
+    for _ in range(20):
+        run()
+    assert counts == [sys.getrefcount(o) for o in (x, w, bias, r, mask, nv, gamma, side, torch.bfloat16, torch.uint8)]
+    monkeypatch.setattr(capi, "_BINDING", _NoFastPath())
+    for a, b in zip(fast, run()):
+        assert torch.equal(a, b)
