@@ -77,11 +77,11 @@ moe_status_t make_linear_maps(CUtensorMap* m, CUtensorMap* tail, int dtype, cons
   return MOE_OK;
 }
 
-// The widest access (16, 4 or 2 bytes) that divides the address and the length
+// The widest access (16, 8, 4 or 2 bytes) that divides the address and the length
 // of every row.
 int row_unit(const void* base, size_t ld, int cols, int es) {
   const size_t all = reinterpret_cast<uintptr_t>(base) | (ld * es) | (static_cast<size_t>(cols) * es);
-  return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : 2;
+  return all % 16 == 0 ? 16 : all % 8 == 0 ? 8 : all % 4 == 0 ? 4 : 2;
 }
 
 struct LinearCall {
@@ -111,7 +111,7 @@ moe_status_t launch_linear_split(const LinearCall& c, int S, cudaStream_t s) {
   return launch_early(kern, ctas, moe::kSplitThreads, L::bytes(n_stages), S, true, s, tw, twt, tx, txt, c.g, S, n_stages);
 }
 
-template <bool FP8, bool PROMOTE, bool SPLIT, bool VEC>
+template <bool FP8, bool PROMOTE, bool SPLIT, int U>
 moe_status_t launch_linear_tile(const LinearCall& c, int tn, int split, cudaStream_t s) {
   using L = moe::TileCfg;
   CUtensorMap tx, txt, tw, twt;
@@ -119,7 +119,7 @@ moe_status_t launch_linear_tile(const LinearCall& c, int tn, int split, cudaStre
   if (r != MOE_OK) return r;
   r = make_linear_maps(&tw, &twt, c.dtype, c.w, c.g.N, c.K, c.ldw, tn / 2);
   if (r != MOE_OK) return r;
-  auto kern = moe::k_linear_tile<FP8, PROMOTE, SPLIT, VEC>;
+  auto kern = moe::k_linear_tile<FP8, PROMOTE, SPLIT, U>;
   static std::atomic<int> attr_set[64];
   r = set_smem_attr(kern, 227 * 1024, attr_set);
   if (r != MOE_OK) return r;
@@ -148,11 +148,14 @@ moe_status_t launch_linear_pairs(LinearCall& c, const LinearPlan& p, cudaStream_
   const int os = float_size(g.out_dt);
   g.out_unit = row_unit(g.out, g.ldo, g.N, os);
   g.res_unit = g.residual ? row_unit(g.residual, g.ldr, g.N, os) : 16;
-  if (p.split > 1) return launch_linear_tile<FP8, PROMOTE, true, false>(c, p.tn, p.split, s);
-  // rows of whole 16-byte units take a kernel without the narrower accesses, which
-  // cost it registers (4096 x 7168 x 512: 35.7 against 41.3 us; an odd N: 49.7)
-  if (g.out_unit == 16 && g.res_unit == 16) return launch_linear_tile<FP8, PROMOTE, false, true>(c, p.tn, 1, s);
-  return launch_linear_tile<FP8, PROMOTE, false, false>(c, p.tn, 1, s);
+  if (p.split > 1) return launch_linear_tile<FP8, PROMOTE, true, 16>(c, p.tn, p.split, s);
+  const int unit = g.out_unit < g.res_unit ? g.out_unit : g.res_unit;
+  if (unit == 16) return launch_linear_tile<FP8, PROMOTE, false, 16>(c, p.tn, 1, s);
+  if (unit == 8) return launch_linear_tile<FP8, PROMOTE, false, 8>(c, p.tn, 1, s);
+  if constexpr (!PROMOTE) {  // fp32 rows are aligned to 4 bytes at least
+    if (unit == 2) return launch_linear_tile<FP8, PROMOTE, false, 2>(c, p.tn, 1, s);
+  }
+  return launch_linear_tile<FP8, PROMOTE, false, 4>(c, p.tn, 1, s);
 }
 
 // Clusters of the pair kernel (2 * split CTAs, one per SM) that run at one time.
@@ -163,7 +166,7 @@ int resident_clusters(int split) {
   std::atomic<int>& slot = cache[dev][split / 2];
   int n = slot.load();
   if (n) return n;
-  auto kern = moe::k_linear_tile<false, false, true, false>;
+  auto kern = moe::k_linear_tile<false, false, true, 16>;
   static std::atomic<int> attr_set[64];
   if (set_smem_attr(kern, 227 * 1024, attr_set) != MOE_OK) return 1;
   cudaLaunchAttribute at[1];

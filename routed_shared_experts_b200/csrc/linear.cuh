@@ -61,7 +61,7 @@ struct LinearArgs {
   int n_tb;    // k_linear_tile: 256-token tiles
   int tn, n_nt;  // k_linear_tile: outputs per tile (a multiple of 32, at most 256), tiles along N
   int split;     // k_linear_tile with SPLIT: pairs along K
-  int out_unit, res_unit;  // k_linear_tile: bytes that divide every row's address and length: 16, 4 or 2
+  int out_unit, res_unit;  // k_linear_tile with SPLIT: bytes that divide every row's address and length: 16, 8, 4 or 2
 };
 
 // Instruction descriptor of kind::f16 with both operands bf16 or both fp16.
@@ -184,31 +184,61 @@ struct SplitOut {
   int n;
   float ws, bias;
 
+  // No condition per value, so that the loads go out together: tokens past t_end
+  // read the last one's.
   template <int C>
   __device__ __forceinline__ void residual(float (&r)[B], int t0, int t_end) const {
+    if (!g.residual || n >= g.N) {
 #pragma unroll
-    for (int i = 0; i < C; ++i)
-      r[i] = g.residual && n < g.N && t0 + i < t_end ? load_residual(g.residual, g.out_dt, (t0 + i) * g.ldr + n) : 0.f;
+      for (int i = 0; i < C; ++i) r[i] = 0.f;
+    } else if (g.out_dt == 4) {
+      const float* p = static_cast<const float*>(g.residual) + n;
+#pragma unroll
+      for (int i = 0; i < C; ++i) r[i] = p[min(t0 + i, t_end - 1) * g.ldr];
+    } else {
+      const unsigned short* p = static_cast<const unsigned short*>(g.residual) + n;
+      unsigned short h[C];
+#pragma unroll
+      for (int i = 0; i < C; ++i) h[i] = p[min(t0 + i, t_end - 1) * g.ldr];
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        r[i] = g.out_dt == 0 ? __bfloat162float(__ushort_as_bfloat16(h[i])) : __half2float(__ushort_as_half(h[i]));
+    }
   }
   __device__ __forceinline__ void residual_of(float (&r)[B], int t0, int t_end) const {
+    if (t_end <= t0) return;  // no tokens in this CTA's share
     if (B == 8 || t_end - t0 <= 8) residual<8>(r, t0, t_end);
     else residual<B>(r, t0, t_end);
   }
   // Scale, bias, activation, residual and store of tokens t0 .. t0 + C - 1.
   template <int C>
   __device__ __forceinline__ void finish(float (&v)[C], const float (&r)[B], int t0, int t_end) const {
-    if (n >= g.N) return;
+    if (n >= g.N || t0 >= t_end) return;
     if (g.x_scale) {
+      float xs[C];
 #pragma unroll
-      for (int i = 0; i < C; ++i)
-        if (t0 + i < t_end) v[i] *= __ldg(g.x_scale + t0 + i) * ws;
+      for (int i = 0; i < C; ++i) xs[i] = __ldg(g.x_scale + min(t0 + i, t_end - 1));
+#pragma unroll
+      for (int i = 0; i < C; ++i) v[i] *= xs[i] * ws;
     }
 #pragma unroll
     for (int i = 0; i < C; ++i) v[i] += bias;
     apply_act(v, g.act);
+    if (g.out_dt == 4) {
+      float* p = static_cast<float*>(g.out) + t0 * g.ldo + n;
 #pragma unroll
-    for (int i = 0; i < C; ++i)
-      if (t0 + i < t_end) store_typed(g.out, g.out_dt, (t0 + i) * g.ldo + n, v[i] + r[i]);
+      for (int i = 0; i < C; ++i)
+        if (t0 + i < t_end) p[i * g.ldo] = v[i] + r[i];
+    } else {
+      unsigned short* p = static_cast<unsigned short*>(g.out) + t0 * g.ldo + n;
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        const float y = v[i] + r[i];
+        const unsigned short h = g.out_dt == 0 ? __bfloat16_as_ushort(__float2bfloat16_rn(y))
+                                               : __half_as_ushort(__float2half_rn(y));
+        if (t0 + i < t_end) p[i * g.ldo] = h;
+      }
+    }
   }
   // Columns c0 .. c0 + C - 1 of the S partial tiles ([token column][128 outputs];
   // `part`: this thread's output of column 0), this CTA's own first, so that the
@@ -486,119 +516,96 @@ struct TileCfg {
 __device__ __forceinline__ int stage_off(int r, int u) { return r * 64 + ((u ^ ((r >> 1) & 3)) << 4); }
 
 // A warp's copies between 32 rows of a matrix, 64 bytes each (`bytes` of them
-// valid, `rows` rows valid), and its staging, in units of U = 16, 4 or 2 bytes:
-// 64 / U lanes take a row, so a copy instruction moves whole row segments
-// whatever their alignment. Register w of a lane holds, for U = 16, word w % 4
-// of the unit of row 8 (w / 4) + lane / 4; for U = 4, row 2 w + lane / 16; for
-// U = 2, rows 2 w and 2 w + 1.
+// valid, `rows` rows valid), and its staging, in units of U = 16, 8, 4 or 2
+// bytes: 64 / U lanes take a row, so a copy instruction moves whole row segments
+// whatever their alignment. A lane's registers hold its units of rows
+// lane * U / 64, + 32 U / 64, ... one after another (U = 2: two to a register).
+// Whole segments are copied without conditions, so that the loads go out together.
+template <int U>
+using unit_t = std::conditional_t<
+    U == 16, uint4, std::conditional_t<U == 8, uint2, std::conditional_t<U == 4, uint32_t, unsigned short>>>;
+
 template <int U>
 __device__ __forceinline__ void fetch_rows(uint32_t (&v)[16], const uint8_t* src, size_t ld, int rows, int bytes,
                                            int lane) {
-  if constexpr (U == 16) {
+  constexpr int kLanes = 64 / U, kRows = 32 / kLanes;  // lanes per row, rows per instruction
+  const int at = lane % kLanes * U, r0 = lane / kLanes;
+  unit_t<U> f[kLanes];
+  src += r0 * ld + at;
+  if (rows >= 32 && bytes == 64) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + (lane >> 2), at = (lane & 3) * 16;
-      uint4 f = make_uint4(0, 0, 0, 0);
-      if (r < rows && at < bytes) f = *reinterpret_cast<const uint4*>(src + r * ld + at);
-      v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
-    }
-  } else if constexpr (U == 4) {
-#pragma unroll
-    for (int w = 0; w < 16; ++w) {
-      const int r = 2 * w + (lane >> 4), at = (lane & 15) * 4;
-      v[w] = r < rows && at < bytes ? *reinterpret_cast<const uint32_t*>(src + r * ld + at) : 0u;
-    }
+    for (int i = 0; i < kLanes; ++i) f[i] = *reinterpret_cast<const unit_t<U>*>(src + kRows * i * ld);
   } else {
-    uint32_t h[32];
-    if (rows >= 32 && bytes == 64) {  // without conditions the loads go out together
 #pragma unroll
-      for (int r = 0; r < 32; ++r) h[r] = *reinterpret_cast<const unsigned short*>(src + r * ld + 2 * lane);
-    } else {
-#pragma unroll
-      for (int r = 0; r < 32; ++r)
-        h[r] = r < rows && 2 * lane < bytes ? *reinterpret_cast<const unsigned short*>(src + r * ld + 2 * lane) : 0u;
+    for (int i = 0; i < kLanes; ++i) {
+      f[i] = unit_t<U>{};
+      if (kRows * i + r0 < rows && at < bytes) f[i] = *reinterpret_cast<const unit_t<U>*>(src + kRows * i * ld);
     }
+  }
 #pragma unroll
-    for (int w = 0; w < 16; ++w) v[w] = h[2 * w] | (h[2 * w + 1] << 16);
+  for (int i = 0; i < kLanes; ++i) {
+    if constexpr (U == 16) v[4 * i] = f[i].x, v[4 * i + 1] = f[i].y, v[4 * i + 2] = f[i].z, v[4 * i + 3] = f[i].w;
+    else if constexpr (U == 8) v[2 * i] = f[i].x, v[2 * i + 1] = f[i].y;
+    else if constexpr (U == 4) v[i] = f[i];
+    else if (i % 2 == 0) v[i / 2] = f[i] | (static_cast<uint32_t>(f[i + 1]) << 16);
   }
 }
 
 template <int U>
 __device__ __forceinline__ void stage_put(uint8_t* st, const uint32_t (&v)[16], int lane) {
-  if constexpr (U == 16) {
+  constexpr int kLanes = 64 / U, kRows = 32 / kLanes;
+  const int at = lane % kLanes * U, r0 = lane / kLanes;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<uint4*>(st + stage_off(8 * i + (lane >> 2), lane & 3)) =
-          make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-  } else if constexpr (U == 4) {
-#pragma unroll
-    for (int w = 0; w < 16; ++w)
-      *reinterpret_cast<uint32_t*>(st + stage_off(2 * w + (lane >> 4), (lane & 15) >> 2) + (lane & 3) * 4) = v[w];
-  } else {
-#pragma unroll
-    for (int w = 0; w < 16; ++w) {
-      const int in = (lane & 7) * 2;
-      *reinterpret_cast<unsigned short*>(st + stage_off(2 * w, lane >> 3) + in) = static_cast<unsigned short>(v[w]);
-      *reinterpret_cast<unsigned short*>(st + stage_off(2 * w + 1, lane >> 3) + in) =
-          static_cast<unsigned short>(v[w] >> 16);
-    }
+  for (int i = 0; i < kLanes; ++i) {
+    uint8_t* to = st + stage_off(kRows * i + r0, at >> 4) + (at & 15);
+    if constexpr (U == 16)
+      *reinterpret_cast<uint4*>(to) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    else if constexpr (U == 8) *reinterpret_cast<uint2*>(to) = make_uint2(v[2 * i], v[2 * i + 1]);
+    else if constexpr (U == 4) *reinterpret_cast<uint32_t*>(to) = v[i];
+    else *reinterpret_cast<unsigned short*>(to) = static_cast<unsigned short>(v[i / 2] >> (16 * (i % 2)));
   }
 }
 
 template <int U>
 __device__ __forceinline__ void stage_store(const uint8_t* st, uint8_t* dst, size_t ld, int rows, int bytes, int lane) {
-  constexpr int kLanes = 64 / U, kRows = 32 / kLanes;  // lanes per row, rows per instruction
-  using TU = std::conditional_t<U == 16, uint4, std::conditional_t<U == 4, uint32_t, unsigned short>>;
+  constexpr int kLanes = 64 / U, kRows = 32 / kLanes;
   const int at = lane % kLanes * U, r0 = lane / kLanes;
-  TU v[kLanes];  // all read before any is stored
+  unit_t<U> v[kLanes];  // all read before any is stored
 #pragma unroll
   for (int i = 0; i < kLanes; ++i)
-    v[i] = *reinterpret_cast<const TU*>(st + stage_off(kRows * i + r0, at >> 4) + (at & 15));
+    v[i] = *reinterpret_cast<const unit_t<U>*>(st + stage_off(kRows * i + r0, at >> 4) + (at & 15));
   dst += r0 * ld + at;
   if (rows >= 32 && bytes == 64) {
 #pragma unroll
-    for (int i = 0; i < kLanes; ++i) *reinterpret_cast<TU*>(dst + kRows * i * ld) = v[i];
+    for (int i = 0; i < kLanes; ++i) *reinterpret_cast<unit_t<U>*>(dst + kRows * i * ld) = v[i];
   } else if (at < bytes) {
 #pragma unroll
     for (int i = 0; i < kLanes; ++i)
-      if (kRows * i + r0 < rows) *reinterpret_cast<TU*>(dst + kRows * i * ld) = v[i];
+      if (kRows * i + r0 < rows) *reinterpret_cast<unit_t<U>*>(dst + kRows * i * ld) = v[i];
   }
 }
 
-// Residual rows of this warp from column n0 (64 bytes of each), by their unit.
-template <int OS, bool VEC>
+// Residual rows of this warp from column n0 (64 bytes of each; OS: bytes of a value).
+template <int OS, int U>
 __device__ __forceinline__ void fetch_residual(const LinearArgs& g, uint32_t (&v)[16], int row0, int n0, int lane) {
-  const uint8_t* src = static_cast<const uint8_t*>(g.residual) + (row0 * g.ldr + n0) * OS;
-  const int bytes = min(64, (g.N - n0) * OS), rows = g.T - row0;
-  if (VEC || g.res_unit == 16) fetch_rows<16>(v, src, g.ldr * OS, rows, bytes, lane);
-  else if (OS == 4 || g.res_unit == 4) fetch_rows<4>(v, src, g.ldr * OS, rows, bytes, lane);
-  else fetch_rows<2>(v, src, g.ldr * OS, rows, bytes, lane);
+  fetch_rows<U>(v, static_cast<const uint8_t*>(g.residual) + (row0 * g.ldr + n0) * OS, g.ldr * OS, g.T - row0,
+                min(64, (g.N - n0) * OS), lane);
 }
 
-template <int OS, bool VEC>
-__device__ __forceinline__ void put_residual(const LinearArgs& g, uint8_t* st, const uint32_t (&v)[16], int lane) {
-  if (VEC || g.res_unit == 16) stage_put<16>(st, v, lane);
-  else if (OS == 4 || g.res_unit == 4) stage_put<4>(st, v, lane);
-  else stage_put<2>(st, v, lane);
-}
-
-template <int OS, bool VEC>
+template <int OS, int U>
 __device__ __forceinline__ void store_result(const LinearArgs& g, const uint8_t* st, int row0, int n0, int lane) {
-  uint8_t* dst = static_cast<uint8_t*>(g.out) + (row0 * g.ldo + n0) * OS;
-  const int bytes = min(64, (g.N - n0) * OS), rows = g.T - row0;
-  if (VEC || g.out_unit == 16) stage_store<16>(st, dst, g.ldo * OS, rows, bytes, lane);
-  else if (OS == 4 || g.out_unit == 4) stage_store<4>(st, dst, g.ldo * OS, rows, bytes, lane);
-  else stage_store<2>(st, dst, g.ldo * OS, rows, bytes, lane);
+  stage_store<U>(st, static_cast<uint8_t*>(g.out) + (row0 * g.ldo + n0) * OS, g.ldo * OS, g.T - row0,
+                 min(64, (g.N - n0) * OS), lane);
 }
 
 // Residual, rounding and store of 32 columns n0.. of this warp's 32 rows
 // (16-bit results): thread = row, through the staging. `res`: the residual
 // fetched ahead (fetch_residual).
-template <typename TX, bool VEC>
+template <typename TX, int U>
 __device__ __forceinline__ void tile_store_16(const LinearArgs& g, uint8_t* st, float (&v)[32],
                                               const uint32_t (&res)[16], int row0, int n0, int lane) {
   if (g.residual) {
-    put_residual<2, VEC>(g, st, res, lane);
+    stage_put<U>(st, res, lane);
     __syncwarp();
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -614,12 +621,12 @@ __device__ __forceinline__ void tile_store_16(const LinearArgs& g, uint8_t* st, 
         make_uint4(pack2(v[8 * u], v[8 * u + 1], TX()), pack2(v[8 * u + 2], v[8 * u + 3], TX()),
                    pack2(v[8 * u + 4], v[8 * u + 5], TX()), pack2(v[8 * u + 6], v[8 * u + 7], TX()));
   __syncwarp();
-  store_result<2, VEC>(g, st, row0, n0, lane);
+  store_result<2, U>(g, st, row0, n0, lane);
   __syncwarp();  // the staging is rewritten next
 }
 
 // The same with fp32 results: two halves of 16 columns (`res`: the first one's).
-template <bool VEC>
+template <int U>
 __device__ __forceinline__ void tile_store_32(const LinearArgs& g, uint8_t* st, float (&v)[32], uint32_t (&res)[16],
                                               int row0, int n0, int lane) {
 #pragma unroll
@@ -627,8 +634,8 @@ __device__ __forceinline__ void tile_store_32(const LinearArgs& g, uint8_t* st, 
     const int c0 = n0 + 16 * h;
     if (c0 >= g.N) return;
     if (g.residual) {
-      put_residual<4, VEC>(g, st, res, lane);
-      if (h == 0 && c0 + 16 < g.N) fetch_residual<4, VEC>(g, res, row0, c0 + 16, lane);  // the second half, meanwhile
+      stage_put<U>(st, res, lane);
+      if (h == 0 && c0 + 16 < g.N) fetch_residual<4, U>(g, res, row0, c0 + 16, lane);  // the second half, meanwhile
       __syncwarp();
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -644,7 +651,7 @@ __device__ __forceinline__ void tile_store_32(const LinearArgs& g, uint8_t* st, 
       *reinterpret_cast<float4*>(st + stage_off(lane, u)) =
           make_float4(v[16 * h + 4 * u], v[16 * h + 4 * u + 1], v[16 * h + 4 * u + 2], v[16 * h + 4 * u + 3]);
     __syncwarp();
-    store_result<4, VEC>(g, st, row0, c0, lane);
+    store_result<4, U>(g, st, row0, c0, lane);
     __syncwarp();
   }
 }
@@ -770,8 +777,10 @@ __device__ __forceinline__ void split_rows(const LinearArgs& g, uint32_t part, u
   }
 }
 
-// VEC: every row of the result and of the residual allows 16-byte accesses.
-template <bool FP8, bool PROMOTE, bool SPLIT, bool VEC>
+// U: the unit of the result's and the residual's rows, a kernel each: one kernel
+// that chose among them ran out of registers (4096 x 7168 x 512: 41.3 against
+// 36.4 us). SPLIT goes by g.out_unit and g.res_unit instead.
+template <bool FP8, bool PROMOTE, bool SPLIT, int U>
 __global__ void __launch_bounds__(kTileThreads, 1)
     k_linear_tile(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXt,
                   const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWt,
@@ -982,7 +991,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const bool in = c < chunks && row0 < g.T && n0 + lane < g.N;
         if (FP8) ws = in ? __ldg(g.w_scale + static_cast<size_t>(n0 + lane) * g.w_scale_step) : 1.f;
         if (g.bias) bias = in ? load_typed(g.bias, g.bias_dt, n0 + lane) : 0.f;
-        if (!PROMOTE && g.residual && c < chunks && row0 < g.T && n0 < g.N) fetch_residual<2, VEC>(g, res, row0, n0, lane);
+        if (!PROMOTE && g.residual && c < chunks && row0 < g.T && n0 < g.N) fetch_residual<2, U>(g, res, row0, n0, lane);
       };
       auto finish = [&](float (&v)[32], int c) {
         const int n0 = nt * g.tn + 32 * c;
@@ -1010,16 +1019,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (!in) return;
         uint32_t r[16];
         if (PROMOTE) {
-          if (g.residual) fetch_residual<4, VEC>(g, r, row0, n0, lane);
+          if (g.residual) fetch_residual<4, U>(g, r, row0, n0, lane);
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) r[i] = res[i];
         }
         fetch(c + 2);
         apply_act(v, g.act);
-        if (PROMOTE) tile_store_32<VEC>(g, st, v, r, row0, n0, lane);
-        else if (g.out_dt == 0) tile_store_16<__nv_bfloat16, VEC>(g, st, v, r, row0, n0, lane);
-        else tile_store_16<__half, VEC>(g, st, v, r, row0, n0, lane);
+        if (PROMOTE) tile_store_32<U>(g, st, v, r, row0, n0, lane);
+        else if (g.out_dt == 0) tile_store_16<__nv_bfloat16, U>(g, st, v, r, row0, n0, lane);
+        else tile_store_16<__half, U>(g, st, v, r, row0, n0, lane);
       };
       fetch(half);
       auto release = [&](int acc) {
