@@ -221,3 +221,62 @@ def test_norm_offsets_past_32_bits(cuda_lib):
     for i, t in enumerate(at):
         assert torch.equal(x[t], want[i])
     assert torch.count_nonzero(x[2:T - 2][::997]).item() == 0
+
+
+def _norm_of_gamma(gamma, quant):
+    """Codes, scales and rows of a row of ones: rms rounds to 1, so the unrounded y is gamma itself."""
+    H = gamma.numel()
+    x = torch.ones((1, H), dtype=torch.bfloat16, device="cuda")
+    codes = torch.empty((1, H), dtype=torch.uint8, device="cuda")
+    scale = torch.empty(1, device="cuda") if quant == "fp8" else torch.empty((1, H // 32), dtype=torch.uint8, device="cuda")
+    capi.moe_rmsnorm_quantize(QUANT[quant], x, None, gamma, 2.0 ** -40, None, None, codes, scale)
+    return codes, scale
+
+
+def test_norm_fp8_codes_match_the_quantiser_at_ties(cuda_lib):
+    """The quotient behind a code is the IEEE one, as moe_quantize_activations
+    has it: 39 / (52 / 448) is 336 exactly, a tie that goes to the even code 320.
+    Whole numbers up to every amax that bf16 holds exactly, both signs and zeros."""
+    H = 512
+    for amax in range(1, 257):
+        gamma = (torch.arange(H, device="cuda") % (2 * amax + 1) - amax).to(torch.bfloat16)
+        gamma[0], gamma[1], gamma[2] = amax, 0.0, -0.0
+        codes, scale = _norm_of_gamma(gamma, "fp8")
+        want, ws = torch.empty_like(codes), torch.empty_like(scale)
+        capi.moe_quantize_activations(QUANT["fp8"], gamma[None], want, ws)
+        assert torch.equal(scale, ws) and torch.equal(codes, want), amax
+
+
+@pytest.mark.parametrize("H", [512, 2048, 7168, 16384])
+def test_norm_fp8_codes_are_of_the_ieee_quotient(cuda_lib, H):
+    """fp32 gamma: y takes any value. Codes equal e4m3(y / s) with the fp32
+    division rounded to nearest, over scales from the subnormal to the largest,
+    values next to ties of the codes, and infinities beside finite values."""
+    g = torch.Generator(device="cuda").manual_seed(H)
+    rand = lambda: torch.rand(H, generator=g, device="cuda")  # noqa: E731
+    mid = torch.tensor([(a + b) / 2 for a, b in zip(_E4M3, _E4M3[1:])], device="cuda")
+    for i in range(60):
+        unit = torch.exp2(torch.tensor(-126.0 + 4.28 * i, device="cuda")) * (1 + rand()[0])
+        s = unit / 448
+        if i % 2:  # ties of the codes times the scale, and their neighbours
+            y = mid[torch.randint(0, mid.numel(), (H,), generator=g, device="cuda")] * s
+            y = y.view(torch.int32).add(torch.randint(-2, 3, (H,), generator=g, device="cuda", dtype=torch.int32)).view(torch.float32)
+        else:
+            y = (rand() * 2 - 1) * unit
+        y[0] = unit
+        if i == 59:
+            y[5] = float("inf")
+        codes, scale = _norm_of_gamma(y, "fp8")
+        amax = y.abs().max()
+        want_s = amax / torch.full_like(amax, 448.0)  # by a tensor: by a number torch multiplies by its reciprocal
+        assert torch.equal(scale[0], want_s), i
+        want = (y / want_s).clamp(-448, 448).to(torch.float8_e4m3fn)
+        got = codes[0].view(torch.float8_e4m3fn)
+        if i == 59:
+            assert torch.isnan(got.float()[5])
+            y[5], want = 0.0, want.float().nan_to_num(0.0).to(torch.float8_e4m3fn)
+            got = got.float().nan_to_num(0.0).to(torch.float8_e4m3fn)
+        assert torch.equal(got.view(torch.uint8), want.view(torch.uint8)), i
+
+
+_E4M3 = sorted({float(v) for v in torch.arange(0, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).float()})
