@@ -5,7 +5,7 @@
         --moe_linear(w_r)--> router logits (fp32) --> the layer
 
 ``MoEBlock`` owns the buffers between the steps and writes the layer's inputs
-(``x``, ``x_scale``, ``logits``) in place, so a step - captured or not - is three
+(``x``, ``x_scale``, ``logits``, and ``x_r`` for the shared gate of an 8-bit layer) in place, so a step - captured or not - is three
 C-ABI calls more than the layer's own. The layer's output is added to the
 residual stream by the next block's norm (``moe_rmsnorm_quantize`` takes the sum
 of its two inputs), not by a kernel of its own.
@@ -15,7 +15,7 @@ from __future__ import annotations
 import torch
 
 from . import capi
-from .layer import capture_forward
+from .layer import capture_forward, gate_rows
 
 
 class MoEBlock:
@@ -41,8 +41,12 @@ class MoEBlock:
         self.quant = None if cfg.dtype == "bf16" else capi.DTYPES["mxfp8" if cfg.dtype in capi.MX_FORMATS else "fp8"]
         if getattr(layer, "quantize_x", False) or getattr(layer, "router_gemm", False):
             raise ValueError("the block quantises x and computes the logits itself")
-        # the router reads the 16-bit rows; a bf16 layer reads the same ones
-        self.y = inp["x"] if self.quant is None else torch.empty((T, H), dtype=torch.bfloat16, device=self.device)
+        # the router reads the 16-bit rows; a bf16 layer reads the same ones, and so does a shared gate
+        if self.quant is None:
+            self.y = inp["x"]
+        else:
+            gated = gate_rows(cfg, inp)
+            self.y = torch.empty((T, H), dtype=torch.bfloat16, device=self.device) if gated is None else gated
         self.o_dt = capi.MOE_DT_BF16 if attn_scale is None else capi.MOE_DT_FP8_E4M3
 
     @property

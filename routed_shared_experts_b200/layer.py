@@ -52,6 +52,19 @@ def route_tokens(cfg: MoEConfig, inp: dict, routing: Routing | None, topk_ids, t
                    stream)
 
 
+def gate_rows(cfg: MoEConfig, inp: dict) -> torch.Tensor | None:
+    """The bf16 activations [T,H] that the shared gate reads (None: no gate):
+    ``x`` of a bf16 layer, ``x_r`` beside the codes of an 8-bit one."""
+    if not cfg.shared_gate:
+        return None
+    if cfg.dtype == "bf16":
+        return inp["x"]
+    x = inp.get("x_r")
+    if x is None or x.dtype != torch.bfloat16 or tuple(x.shape) != (cfg.T, cfg.H):
+        raise ValueError("the shared gate of a layer with 8-bit x reads its bf16 rows: inp['x_r'] of shape [T, H]")
+    return x
+
+
 def capture_forward(layer, stream=None, steps: int = 1) -> torch.cuda.CUDAGraph:
     """A CUDA graph of ``steps`` consecutive ``layer.forward(stream)`` calls.
 
@@ -83,7 +96,8 @@ class MoELayer:
     ``self.logits``. With ``quantize_x`` (fp8 / MXFP8 layers) the step starts
     from the bf16 activations ``x_r``: ``moe_quantize_activations`` writes
     ``self.xq`` / ``self.xq_scale``, which both GEMM paths then read instead
-    of ``x`` / ``x_scale``. With ``routing`` the experts are chosen by
+    of ``x`` / ``x_scale``. The shared gate of an fp8 or MX layer reads the bf16
+    activations ``x_r``. With ``routing`` the experts are chosen by
     ``moe_route`` (see ``Routing``) instead of the config's routing mode.
     """
 
@@ -149,8 +163,8 @@ class MoELayer:
         ws1s = capi.stage1_workspace_bytes(self.dt, T, 1, 1, H, Is, bm)
         self.ws1 = torch.zeros(ws1, dtype=torch.uint8, device=dev) if ws1 else None  # zeroed once
         self.ws1_s = torch.zeros(ws1s, dtype=torch.uint8, device=dev) if ws1s else None
-        gdt = torch.bfloat16 if cfg.dtype == "bf16" else torch.float16
-        self.gate = torch.empty(T, dtype=gdt, device=dev) if cfg.shared_gate else None
+        gate_rows(cfg, inp)  # refused here rather than at the first step
+        self.gate = torch.empty(T, dtype=torch.bfloat16, device=dev) if cfg.shared_gate else None
         self.addend = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
         self.out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
         ws = capi.stage2_workspace_bytes(T, H)
@@ -172,7 +186,7 @@ class MoELayer:
         cfg, inp = self.cfg, self.inp
         T, H, Is = cfg.T, cfg.H, cfg.Is
         if self.gate is not None:
-            capi.shared_expert_gate_dot(capi.MOE_DT_BF16, inp["x"], inp["w_gate"], True, self.gate, stream)
+            capi.shared_expert_gate_dot(capi.MOE_DT_BF16, gate_rows(cfg, inp), inp["w_gate"], True, self.gate, stream)
         capi.moe_stage1_gemm(self.dt, *self._x(), inp["w13s"], self.wsc["w13s"],
                              None, None, None, T, 1, H, Is, 1, self.bm, self.h_s, self.h_scale_s, self.ws1_s, stream)
         wdt = capi.MOE_DT_BF16 if self.gate is not None else capi.MOE_DT_F32
@@ -333,6 +347,7 @@ class FusedSharedMoELayer:
                                        device=dev)
         ws1 = capi.stage1_workspace_bytes(self.dt, T, self.k2, self.E2, H, I, bm)
         self.ws1 = torch.zeros(ws1, dtype=torch.uint8, device=dev) if ws1 else None  # zeroed once
+        gate_rows(cfg, inp)
         self.gate = torch.empty(T, dtype=torch.bfloat16, device=dev) if cfg.shared_gate else None
         self.out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
         self.acc_ws = torch.zeros(capi.stage2_workspace_bytes(T, H) // 4, dtype=torch.float32, device=dev)
@@ -344,7 +359,7 @@ class FusedSharedMoELayer:
         T, H, E, k, I = cfg.T, cfg.H, cfg.E, cfg.top_k, cfg.I
         s = stream or torch.cuda.current_stream(self.device)
         if self.gate is not None:
-            capi.shared_expert_gate_dot(capi.MOE_DT_BF16, inp["x"], inp["w_gate"], True, self.gate, s)
+            capi.shared_expert_gate_dot(capi.MOE_DT_BF16, gate_rows(cfg, inp), inp["w_gate"], True, self.gate, s)
         route_tokens(cfg, inp, self.routing, self.topk_ids, self.topk_weights, s)
         capi.moe_append_shared_slots(self.topk_ids, self.topk_weights, E, self.m, self.gate, self.ids2,
                                      self.w2slots, s)

@@ -232,3 +232,33 @@ def test_both_paths_of_the_wrappers_agree(cuda_lib, monkeypatch):
     monkeypatch.setattr(capi, "_BINDING", _NoFastPath())
     for a, b in zip(fast, run()):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("case", [2, 3, 4])
+def test_block_gated_8_bit_layers(cuda_lib, case):
+    """The gate reads the norm's 16-bit rows beside the codes. Against the same
+    layer without a gate: a = bf16(g * y) and a0 = bf16(y) are each off by half a
+    step, 2^-8, and the gate's own product in fp32 by 2^-23."""
+    base, kw, kind, attn_fp8 = CASES[case]
+    cfg = _cfg(base, dict(kw, shared_gate=True), f"gated{case}")
+    block = _make(cfg, kind, attn_fp8=attn_fp8)
+    layer = block.layer
+    res0 = block.residual.clone()
+    block.forward()
+    torch.cuda.synchronize()
+    assert capi.device_error() == 0
+    _check_front(block, res0)
+    assert block.y is layer.inp["x_r"]
+    ref = oracle.shared_gate(block.y.cpu().double().numpy(), layer.inp["w_gate"].cpu().double().numpy(), True, oracle.BF16)
+    g = layer.gate.cpu().double().numpy()
+    assert np.all(np.abs(g - ref) <= 2.0 ** -7 * ref)  # neighbours of one rounding
+    plain = kind(configs.small(cfg, shared_gate=False), layer.inp)
+    plain.forward()
+    torch.cuda.synchronize()
+    gd = layer.gate.double()[:, None]
+    if kind is MoELayer:
+        want = plain.addend.double() * gd
+        assert torch.all((layer.addend.double() - want).abs() <= (2.0 ** -7 + 2.0 ** -14) * want.abs() + 2.0 ** -126)
+    else:
+        assert torch.equal(layer.w2slots[:, cfg.top_k:], layer.gate.float()[:, None].expand(-1, layer.m))
+    assert torch.equal(layer.topk_ids, plain.topk_ids) and not torch.equal(layer.out, plain.out)
