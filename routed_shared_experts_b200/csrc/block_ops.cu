@@ -310,7 +310,7 @@ moe_status_t moe_linear(int dtype, const void* x, int64_t ldx, const float* x_sc
   if (ldx < K || ldw < K || ldo < N || (residual && ldr < N)) return MOE_ERR_INVALID_ARG;
   const int es = fp8 ? 1 : 2;
   const int64_t row_max = int64_t{1} << 36;  // row strides the tensor maps and 64-bit offsets cover
-  const int size_max = 1 << 30;              // and sizes whose last tile still counts in 32 bits
+  const int size_max = 1 << 30;              // and sizes whose tiles count in 32 bits, past the last one included
   if (T > size_max || N > size_max || K > size_max) return MOE_ERR_SHAPE;
   if (ldx > row_max || ldw > row_max || ldo > row_max || (residual && ldr > row_max)) return MOE_ERR_SHAPE;
   const int os = float_size(out_dtype);

@@ -585,17 +585,24 @@ __device__ __forceinline__ void stage_store(const uint8_t* st, uint8_t* dst, siz
   }
 }
 
+// Valid bytes of a row's 64 from column n0 < N on. Counted in columns first: N - n0
+// times the value's size passes 31 bits from N = 2^29 (fp32) on.
+template <int OS>
+__host__ __device__ constexpr int chunk_bytes(int N, int n0) {
+  return (N - n0 < 64 / OS ? N - n0 : 64 / OS) * OS;
+}
+
 // Residual rows of this warp from column n0 (64 bytes of each; OS: bytes of a value).
 template <int OS, int U>
 __device__ __forceinline__ void fetch_residual(const LinearArgs& g, uint32_t (&v)[16], int row0, int n0, int lane) {
   fetch_rows<U>(v, static_cast<const uint8_t*>(g.residual) + (row0 * g.ldr + n0) * OS, g.ldr * OS, g.T - row0,
-                min(64, (g.N - n0) * OS), lane);
+                chunk_bytes<OS>(g.N, n0), lane);
 }
 
 template <int OS, int U>
 __device__ __forceinline__ void store_result(const LinearArgs& g, const uint8_t* st, int row0, int n0, int lane) {
   stage_store<U>(st, static_cast<uint8_t*>(g.out) + (row0 * g.ldo + n0) * OS, g.ldo * OS, g.T - row0,
-                 min(64, (g.N - n0) * OS), lane);
+                 chunk_bytes<OS>(g.N, n0), lane);
 }
 
 // Residual, rounding and store of 32 columns n0.. of this warp's 32 rows

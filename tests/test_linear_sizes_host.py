@@ -1,0 +1,47 @@
+"""Arithmetic of moe_linear's kernels at the largest sizes it accepts, run on the
+host: the functions are those of the kernels' header."""
+import os
+import subprocess
+
+import pytest
+
+from routed_shared_experts_b200 import build
+
+SRC = r"""
+#include "linear.cuh"
+#include <cstdio>
+
+template <int OS>
+int check() {
+  int bad = 0;
+  const int sizes[] = {1, 15, 16, 17, 31, 32, 33, 1000, (1 << 28) - 1, 1 << 28, (1 << 29) - 1, 1 << 29, (1 << 29) + 1,
+                       (1 << 30) - 1, 1 << 30};
+  for (const int N : sizes)
+    for (long long back = 0; back < N; back = back < 70 ? back + 1 : back * 2) {
+      for (const long long n0 : {back, N - 1 - back}) {
+        if (n0 % (64 / OS) != 0) continue;  // chunks start on whole 64-byte columns
+        const long long left = (N - n0) * OS;
+        const int want = static_cast<int>(left < 64 ? left : 64);
+        const int got = moe::chunk_bytes<OS>(N, static_cast<int>(n0));
+        if (got != want && bad++ < 5) printf("OS %d N %d n0 %lld: %d, expected %d\n", OS, N, n0, got, want);
+      }
+    }
+  return bad;
+}
+
+int main() { return check<2>() + check<4>() ? 1 : 0; }
+"""
+
+
+def test_chunk_bytes_up_to_the_largest_rows(tmp_path):
+    """Bytes of a 64-byte chunk that a row of N values holds: T > 64 rows of 2^29
+    fp32 results (140 GB) fit a GPU, and their chunks are whole."""
+    src = tmp_path / "sizes.cu"
+    src.write_text(SRC)
+    exe = tmp_path / "sizes"
+    cmd = [build._nvcc(), "-O1", "-std=c++17", *build.ARCH, "-cudart", "static", "-I", build.INCLUDE, "-I", build.CSRC,
+           "-o", str(exe), str(src)]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr
+    run = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert run.returncode == 0, run.stdout
