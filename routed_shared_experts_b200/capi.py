@@ -341,6 +341,8 @@ def moe_linear(dtype, x, x_scale, w, w_scale, bias, act, residual, out, stream=N
         bias_dt = _FLOAT_DT[bias.dtype]
     if w_scale is not None:
         ws_rows = w_scale.numel()
+        if not ws_rows:  # its null address would read as no scale
+            raise ValueError("w_scale has no elements")
     status = (_LIB or lib()).moe_linear(
         dtype, x.data_ptr(), ldx, _vec(x_scale, "x_scale", T, _F32), w.data_ptr(), ldw,
         _vec(w_scale, "w_scale", ws_rows, _F32), ws_rows, pb, bias_dt, act, pr, ldr, out.data_ptr(),

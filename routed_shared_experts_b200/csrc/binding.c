@@ -86,13 +86,14 @@ static int operand(PyObject* t, long long dev, tensor_t* o) {
   return o->ld >= o->cols;
 }
 
-/* a dense tensor of any shape; None: a null pointer */
+/* a dense tensor of any shape with elements; None: a null pointer (which an empty
+ * tensor's address would be too) */
 static int vector(PyObject* t, long long dev, tensor_t* o) {
   o->ptr = NULL;
   o->rows = 0;
   o->type = -1;
   if (t == Py_None) return 1;
-  if (!common(t, dev, o) || !long_of(PyObject_CallMethodNoArgs(t, s_numel), &o->rows)) return 0;
+  if (!common(t, dev, o) || !long_of(PyObject_CallMethodNoArgs(t, s_numel), &o->rows) || o->rows < 1) return 0;
   PyObject* c = PyObject_CallMethodNoArgs(t, s_is_contiguous);
   const int ok = c == Py_True;
   Py_XDECREF(c);
