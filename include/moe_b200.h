@@ -480,8 +480,9 @@ moe_status_t moe_linear(int dtype, const void* x, int64_t ldx, const float* x_sc
  *     s = softmax(l) over the live experts, or sigmoid(l); in double,
  *     c = fp32(s) + bias                      (what the choice goes by)
  *     group score = sum of the two largest c of the group's live experts (one
- *         if only one lives), or the largest; the topk_group best groups are
- *         kept (ties: lower group)
+ *         if only one lives), or the largest, in fp32 (a sum below its range
+ *         counts as its lowest value); the topk_group best groups are kept
+ *         (ties: lower group; groups in which nothing lives last)
  *     the top_k largest c of the kept groups are picked (ties: lower index)
  *     w_j = s_j / sum of the picked s (renormalize != 0), or s_j; times
  *         routed_scaling_factor; rounded once.

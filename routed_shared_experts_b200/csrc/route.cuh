@@ -201,8 +201,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
       m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
       m1 = fmaxf(m1, o1);
     }
-    // a group with one live expert scores that expert alone
-    const float score = (a.group_max || m2 == NEG_INF) ? m1 : __fadd_rn(m1, m2);
+    // a group with one live expert scores that expert alone; two whose sum lies below the fp32 range (biases of
+    // its lowest value) still score above a group without one
+    const float score = (a.group_max || m2 == NEG_INF) ? m1 : fmaxf(__fadd_rn(m1, m2), -3.402823466e38f);
     uint32_t gkey = (sub == 0 && g < a.n_group) ? order_key(score) : 0;
     uint32_t kept = 0;  // by group
     for (int r = 0; r < a.topk_group; ++r) {

@@ -256,3 +256,28 @@ def test_padding_rows_take_no_shared_slots(cuda_lib):
     torch.cuda.synchronize()
     assert oi[:4, k:].cpu().tolist() == [[8, 9, 10]] * 4 and torch.all(ow[:4, k:] == 0.25)
     assert torch.all(oi[4:] == capi.MOE_NO_EXPERT) and torch.all(ow[4:, k:] == 0)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_live_group_below_the_fp32_range(cuda_lib, score):
+    """A bias of the type's lowest value masks experts without switching them
+    off. Two of them add up below the fp32 range: their group still counts more
+    than one in which nothing lives, whatever the order of the groups."""
+    low = torch.finfo(torch.float32).min
+    E, G = 32, 4
+    logits = torch.from_numpy(np.random.default_rng(8).normal(0, 1, (5, E)).astype(np.float32))
+    for dead, alive in ((0, 2), (3, 1)):
+        bias = np.full(E, low, np.float32)
+        mask = np.ones(E, np.uint8)
+        mask[dead * 8:dead * 8 + 8] = 0
+        others = [g for g in range(G) if g not in (dead, alive)]
+        for g in others:
+            bias[g * 8:g * 8 + 8] = 0.0
+        dev = logits.cuda()
+        ids = torch.empty((5, 20), dtype=torch.int32, device="cuda")
+        w = torch.empty((5, 20), device="cuda")
+        capi.moe_route(dev, torch.from_numpy(bias).cuda(), torch.from_numpy(mask).cuda(), None, 20, capi.SCORES[score],
+                       G, 3, capi.MOE_GROUP_TOP2, False, 1.0, ids, w)
+        got = ids.cpu() // 8
+        assert set(got.unique().tolist()) == set(others + [alive])
+        assert torch.all(w > 0)  # all twenty picks live
