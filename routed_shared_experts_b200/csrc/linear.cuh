@@ -5,7 +5,9 @@
 // x [T, K] and w [N, K] are read by TMA in 128-byte K atoms (64 values of 16
 // bits, 128 of 8; the tensor map zero-fills past K, T and N, so any T, N and K
 // runs), the sum is kept in fp32 in TMEM, everything after it happens in
-// registers, and the result is rounded once.
+// registers, and the result is rounded once. The scales are applied one after
+// the other: their own product could leave the fp32 range where the result does
+// not.
 //
 // A pipeline stage holds kLinAtoms K atoms, and two producer warps load one
 // operand each, with one copy per stage: the map views the operand as
@@ -219,7 +221,7 @@ struct SplitOut {
 #pragma unroll
       for (int i = 0; i < C; ++i) xs[i] = __ldg(g.x_scale + min(t0 + i, t_end - 1));
 #pragma unroll
-      for (int i = 0; i < C; ++i) v[i] *= xs[i] * ws;
+      for (int i = 0; i < C; ++i) v[i] = v[i] * xs[i] * ws;
     }
 #pragma unroll
     for (int i = 0; i < C; ++i) v[i] += bias;
@@ -774,7 +776,7 @@ __device__ __forceinline__ void split_rows(const LinearArgs& g, uint32_t part, u
         const int t = t0 + r0 + j;
         if (t >= g.T) break;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[j][i] = v[j][i] * (xs[j] * ws[i]) + bias[i];
+        for (int i = 0; i < 4; ++i) v[j][i] = v[j][i] * xs[j] * ws[i] + bias[i];
         apply_act(v[j], g.act);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[j][i] += res[j][i];
@@ -1011,10 +1013,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int i = 0; i < 8; ++i) {
           if (FP8) {
             const float4 w = reinterpret_cast<const float4*>(vec)[i];
-            v[4 * i] *= xs * w.x;
-            v[4 * i + 1] *= xs * w.y;
-            v[4 * i + 2] *= xs * w.z;
-            v[4 * i + 3] *= xs * w.w;
+            v[4 * i] = v[4 * i] * xs * w.x;
+            v[4 * i + 1] = v[4 * i + 1] * xs * w.y;
+            v[4 * i + 2] = v[4 * i + 2] * xs * w.z;
+            v[4 * i + 3] = v[4 * i + 3] * xs * w.w;
           }
           const float4 b = reinterpret_cast<const float4*>(vec)[8 + i];
           v[4 * i] += b.x;

@@ -291,3 +291,27 @@ def test_linear_offsets_past_32_bits(cuda_lib, T, gap):
     assert capi.device_error() == 0
     ref = (x.double() @ w.double().t() + r.double()).to(torch.bfloat16)
     assert torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("T,N,K", [(3, 40, 256), (40, 300, 2048), (130, 96, 7168), (300, 520, 256), (1024, 1024, 512)])
+@pytest.mark.parametrize("odt", ["f32", "bf16"])
+def test_linear_scales_far_apart(cuda_lib, T, N, K, odt):
+    """The sum is scaled by token and then by output, as the formula has it: a
+    pair of scales whose own product leaves the fp32 range costs nothing where
+    the result does not. Powers of two and whole numbers, so one rounding."""
+    g = torch.Generator().manual_seed(T)
+    x, w = (torch.randint(-3, 4, (n, K), generator=g).float().to(DT["fp8"]) for n in (T, N))
+    ref = x.double() @ w.double().t()
+    for ex, ew in ((-100, -40), (-100, -60), (-90, -58), (90, -100), (100, 60)):
+        xs, ws = torch.full((T,), 2.0 ** ex), torch.full((N,), 2.0 ** ew)
+        if ex + ew > 127:  # only zeros stay in range: 0 * scale is 0
+            xz = torch.zeros((T, K)).to(DT["fp8"])
+            want, xv = torch.zeros((T, N), dtype=torch.float64), xz
+        else:
+            want, xv = ref * 2.0 ** (ex + ew), x
+        out = torch.full((T, N), 7.0, dtype=DT[odt], device="cuda")
+        capi.moe_linear(capi.MOE_DT_FP8_E4M3, xv.cuda(), xs.cuda(), w.cuda(), ws.cuda(), None, 0, None, out)
+        if odt == "f32":
+            assert torch.equal(out.cpu(), want.float()), (ex, ew)
+        else:  # fp32 first (exact down to its subnormal step), then the result type
+            assert torch.equal(out.cpu(), want.float().to(DT[odt])), (ex, ew)
