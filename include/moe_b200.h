@@ -457,9 +457,13 @@ moe_status_t shared_expert_gate_dot(int dtype, const void* x, const void* w, int
  *   x_scale    fp32 [T] and w_scale fp32 [w_scale_rows], w_scale_rows = N (one
  *              per output) or 1 (one per matrix): FP8 only, NULL otherwise.
  *   bias       [N] of bias_dtype (BF16, FP16, F32), or NULL.
- *   act        MOE_ACT_*, evaluated in fp32 with the fast exponential
- *              (relative error near 2^-21; GELU's error function adds
- *              2^-24 |v|); NaN and infinities follow the formula.
+ *   act        MOE_ACT_*, evaluated in fp32. SiLU, sigmoid and tanh-GELU, whose
+ *              exponential has the argument u = v (tanh-GELU: twice the tanh's):
+ *              relative error 2^-20 for fp32 results, (4 + 1.2 |u|) 2^-23 for
+ *              16-bit ones (far below their own rounding; results under 2^-119
+ *              may be 0); tanh-GELU's u is itself rounded, 7 |u| 2^-24 more.
+ *              GELU's error function adds 2^-24 |v|. NaN and infinities follow
+ *              the formula.
  *   residual   [T,N] of out_dtype, rows ldr apart, or NULL. It may be out
  *              itself (same address and stride); any other overlap of out
  *              with an operand is undefined.

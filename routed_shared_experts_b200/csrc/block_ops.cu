@@ -92,7 +92,7 @@ struct LinearCall {
   moe::LinearArgs g;
 };
 
-template <int BN, bool FP8>
+template <int BN, bool FP8, bool F32>
 moe_status_t launch_linear_split(const LinearCall& c, int S, cudaStream_t s) {
   using L = moe::SplitCfg<BN>;
   CUtensorMap tw, twt, tx, txt;
@@ -100,7 +100,7 @@ moe_status_t launch_linear_split(const LinearCall& c, int S, cudaStream_t s) {
   if (r != MOE_OK) return r;
   r = make_linear_maps(&tx, &txt, c.dtype, c.x, c.g.T, c.K, c.ldx, BN);
   if (r != MOE_OK) return r;
-  auto kern = moe::k_linear_split<BN, FP8>;
+  auto kern = moe::k_linear_split<BN, FP8, F32>;
   static std::atomic<int> attr_set[64];
   r = set_smem_attr(kern, 227 * 1024, attr_set);
   if (r != MOE_OK) return r;
@@ -237,14 +237,13 @@ LinearPlan plan_linear(int T, int N, int nk, bool f32_out) {
   return p;
 }
 
-template <bool FP8>
+template <bool FP8, bool F32>
 moe_status_t launch_linear(LinearCall& c, cudaStream_t s) {
-  const bool f32 = c.g.out_dt == MOE_DT_F32;
-  const LinearPlan p = plan_linear(c.g.T, c.g.N, c.g.nk, f32);
-  if (p.tn) return f32 ? launch_linear_pairs<FP8, true>(c, p, s) : launch_linear_pairs<FP8, false>(c, p, s);
-  if (p.bn == 16) return launch_linear_split<16, FP8>(c, p.split, s);
-  if (p.bn == 32) return launch_linear_split<32, FP8>(c, p.split, s);
-  return launch_linear_split<64, FP8>(c, p.split, s);
+  const LinearPlan p = plan_linear(c.g.T, c.g.N, c.g.nk, F32);
+  if (p.tn) return launch_linear_pairs<FP8, F32>(c, p, s);
+  if (p.bn == 16) return launch_linear_split<16, FP8, F32>(c, p.split, s);
+  if (p.bn == 32) return launch_linear_split<32, FP8, F32>(c, p.split, s);
+  return launch_linear_split<64, FP8, F32>(c, p.split, s);
 }
 
 template <int VPL>
@@ -342,7 +341,9 @@ moe_status_t moe_linear(int dtype, const void* x, int64_t ldx, const float* x_sc
   g.out = out;
   g.ldo = static_cast<size_t>(ldo);
   g.out_dt = out_dtype;
-  return fp8 ? launch_linear<true>(c, as_stream(stream)) : launch_linear<false>(c, as_stream(stream));
+  cudaStream_t s = as_stream(stream);
+  if (out_dtype == MOE_DT_F32) return fp8 ? launch_linear<true, true>(c, s) : launch_linear<false, true>(c, s);
+  return fp8 ? launch_linear<true, false>(c, s) : launch_linear<false, false>(c, s);
 }
 
 moe_status_t moe_route(const void* logits, int logits_dtype, int64_t ld, const float* bias,

@@ -71,10 +71,24 @@ __host__ __device__ constexpr uint32_t idesc_16bit(int M, int N, bool f16) {
   return f16 ? idesc_bf16(M, N) & ~((7u << 7) | (7u << 10)) : idesc_bf16(M, N);
 }
 
-// The activation of C accumulated values. The exponentials are the fast ones
-// (relative error near 2^-21, far below a 16-bit output's rounding and of the
-// size of the fp32 accumulation's own error). NaN passes through every one.
-template <int C>
+// num * sigmoid(v). ACCURATE (fp32 results): by e = exp(-|v|) in (0, 1], so that
+// nothing overflows and the left tail keeps its relative precision down to the
+// subnormals; the library's expf (2^-22) and a division by 1 + e in [1, 2] (2^-22)
+// leave 2^-20 with the roundings beside them. Else (16-bit results) num / (1 + exp(-v))
+// with the fast exponential, ex2 of the rounded product v log2(e): (4 + 1.2 |v|) 2^-23,
+// far below the store's half step, and zeros in place of results below 2^-119, where
+// the fast division's divisor passes 2^126. The accurate form costs fp32 results 2 to
+// 8 % (4096 x 256 x 7168 SiLU 23.0 -> 23.5 us, 777 x 2815 x 4096 tanh-GELU 38.5 ->
+// 41.7) and would cost 16-bit ones, whose store hides the difference, 3 %.
+template <bool ACCURATE>
+__device__ __forceinline__ float times_sigmoid(float num, float v) {
+  if (!ACCURATE) return __fdividef(num, 1.0f + __expf(-v));
+  const float e = expf(-fabsf(v));
+  return num * __fdividef(v < 0.f ? e : 1.0f, 1.0f + e);
+}
+
+// The activation of C accumulated values. NaN passes through every one.
+template <bool ACCURATE, int C>
 __device__ __forceinline__ void apply_act(float (&v)[C], int act) {
   switch (act) {
     case kActRelu:
@@ -83,23 +97,23 @@ __device__ __forceinline__ void apply_act(float (&v)[C], int act) {
       break;
     case kActSilu:
 #pragma unroll
-      for (int i = 0; i < C; ++i) v[i] = __fdividef(v[i], 1.0f + __expf(-v[i]));
+      for (int i = 0; i < C; ++i) v[i] = times_sigmoid<ACCURATE>(v[i], v[i]);
       break;
     case kActGelu:  // v * Phi(v). erff against erfcf(-x): 23 against 31 us at 777 x 2815 x 4096, for an
                     // absolute error of 2^-24 |v| in the left tail, where the result itself vanishes
 #pragma unroll
       for (int i = 0; i < C; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(0.70710678118654752f * v[i]));
       break;
-    case kActGeluTanh:  // 0.5 v (1 + tanh u) = v / (1 + exp(-2u))
+    case kActGeluTanh:  // 0.5 v (1 + tanh u) = v sigmoid(2u)
 #pragma unroll
       for (int i = 0; i < C; ++i) {
         const float u2 = 1.5957691216057308f * (v[i] + 0.044715f * v[i] * v[i] * v[i]);
-        v[i] = __fdividef(v[i], 1.0f + __expf(-u2));
+        v[i] = times_sigmoid<ACCURATE>(v[i], u2);
       }
       break;
     case kActSigmoid:
 #pragma unroll
-      for (int i = 0; i < C; ++i) v[i] = __fdividef(1.0f, 1.0f + __expf(-v[i]));
+      for (int i = 0; i < C; ++i) v[i] = times_sigmoid<ACCURATE>(1.0f, v[i]);
       break;
     default: break;
   }
@@ -124,9 +138,18 @@ __device__ __forceinline__ void store_typed(void* p, int dt, size_t i, float v) 
   else static_cast<__half*>(p)[i] = __float2half_rn(v);
 }
 
-__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr) {
+// 0 where `on` is false. A predicate rather than a branch, so that a batch of
+// loads goes out together.
+__device__ __forceinline__ float ld_shared_cluster_f32_if(uint32_t cluster_addr, bool on) {
   float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %2, 0;\n\t"
+      "mov.f32 %0, 0f00000000;\n\t"
+      "@p ld.shared::cluster.f32 %0, [%1];\n\t}\n"
+      : "=f"(v)
+      : "r"(cluster_addr), "r"(static_cast<int>(on))
+      : "memory");
   return v;
 }
 
@@ -180,7 +203,9 @@ struct SplitCfg {
 // residual, K = 7168: 22.6 -> 20.6 us for 32 tokens against batches of 8 alone;
 // N = 2048, one token: 5.5 us against 6.8 with batches of 16 alone). Tiles of 16
 // tokens have no use for the wider batch, whose registers cost them 0.3 us.
-template <int B>  // widest batch: 8 or 16
+// F32: fp32 results, a kernel each, so that the code of one result type is all that a launch
+// of a few microseconds fetches.
+template <int B, bool F32>  // B: widest batch, 8 or 16
 struct SplitOut {
   const LinearArgs& g;
   int n;
@@ -193,7 +218,7 @@ struct SplitOut {
     if (!g.residual || n >= g.N) {
 #pragma unroll
       for (int i = 0; i < C; ++i) r[i] = 0.f;
-    } else if (g.out_dt == 4) {
+    } else if (F32) {
       const float* p = static_cast<const float*>(g.residual) + n;
 #pragma unroll
       for (int i = 0; i < C; ++i) r[i] = p[min(t0 + i, t_end - 1) * g.ldr];
@@ -225,8 +250,8 @@ struct SplitOut {
     }
 #pragma unroll
     for (int i = 0; i < C; ++i) v[i] += bias;
-    apply_act(v, g.act);
-    if (g.out_dt == 4) {
+    apply_act<F32>(v, g.act);
+    if (F32) {
       float* p = static_cast<float*>(g.out) + t0 * g.ldo + n;
 #pragma unroll
       for (int i = 0; i < C; ++i)
@@ -256,13 +281,13 @@ struct SplitOut {
       const uint32_t peer = mapa_shared(part, static_cast<uint32_t>((rank + p) & (S - 1)));
 #pragma unroll
       for (int i = 0; i < C; ++i)
-        if (c0 + i < c_hi) v[i] += ld_shared_cluster_f32(peer + static_cast<uint32_t>((c0 + i) * kTileM * 4));
+        v[i] += ld_shared_cluster_f32_if(peer + static_cast<uint32_t>((c0 + i) * kTileM * 4), c0 + i < c_hi);
     }
     finish(v, r, c0, c_hi);
   }
 };
 
-template <int BN, bool FP8>
+template <int BN, bool FP8, bool F32>
 __global__ void __launch_bounds__(kSplitThreads)
     k_linear_split(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWt,
                    const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXt,
@@ -389,7 +414,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   // S > 1: this CTA finishes columns c_lo .. c_hi - 1
   const int c_lo = nv * rank / S, c_hi = nv * (rank + 1) / S;
   constexpr int B = BN == 16 ? 8 : 16;
-  SplitOut<B> o{g, n, 0.f, 0.f};
+  SplitOut<B, F32> o{g, n, 0.f, 0.f};
   float res[B];
   bool ok = false;
   if (warp >= 3) {
@@ -731,6 +756,7 @@ __device__ __forceinline__ void store4(const LinearArgs& g, size_t at, int cols,
   }
 }
 
+template <bool F32>
 __device__ __forceinline__ void split_rows(const LinearArgs& g, uint32_t part, uint32_t ctarank, int mt, int nt, int ew,
                                            int lane) {
   const int S = g.split;
@@ -777,7 +803,7 @@ __device__ __forceinline__ void split_rows(const LinearArgs& g, uint32_t part, u
         if (t >= g.T) break;
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[j][i] = v[j][i] * xs[j] * ws[i] + bias[i];
-        apply_act(v[j], g.act);
+        apply_act<F32>(v[j], g.act);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[j][i] += res[j][i];
         store4(g, t * g.ldo + n, cols, v[j]);
@@ -1034,7 +1060,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int i = 0; i < 16; ++i) r[i] = res[i];
         }
         fetch(c + 2);
-        apply_act(v, g.act);
+        apply_act<PROMOTE>(v, g.act);
         if (PROMOTE) tile_store_32<U>(g, st, v, r, row0, n0, lane);
         else if (g.out_dt == 0) tile_store_16<__nv_bfloat16, U>(g, st, v, r, row0, n0, lane);
         else tile_store_16<__half, U>(g, st, v, r, row0, n0, lane);
@@ -1095,7 +1121,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (warp >= 3) {
       int mt, nt;
       tile_coords(g, unit0, mt, nt);
-      split_rows(g, smem_u32(stages), ctarank, mt, nt, warp - 3, lane);
+      split_rows<PROMOTE>(g, smem_u32(stages), ctarank, mt, nt, warp - 3, lane);
     }
   }
   tc_fence_before();

@@ -315,3 +315,62 @@ def test_linear_scales_far_apart(cuda_lib, T, N, K, odt):
             assert torch.equal(out.cpu(), want.float()), (ex, ew)
         else:  # fp32 first (exact down to its subnormal step), then the result type
             assert torch.equal(out.cpu(), want.float().to(DT[odt])), (ex, ew)
+
+
+@pytest.mark.parametrize("act", ["silu", "sigmoid", "gelu_tanh"])
+@pytest.mark.parametrize("T,N,K", [(4, 1024, 64), (40, 1024, 64), (300, 1024, 64), (66, 1024, 4096)])
+def test_linear_activations_over_the_exponentials_range(cuda_lib, act, T, N, K):
+    """Pre-activations from -80 to 80 that the sum gives exactly (one product of
+    a power of two and a bf16 value per output), fp32 results.
+
+    The exponential of an exact argument is within 2 units of the last place
+    (2^-22), the sum 1 + e and the quotient within 2^-24 and 2^-23, a product with
+    v 2^-24: 2^-20 in all. GELU's exponent is rounded itself: v^2, the cubic
+    term, the sum and two products leave 6 roundings of 2^-24 relative, that is
+    6 * 2^-24 |u| in the exponential, u = 2 sqrt(2/pi) (v + 0.044715 v^3); the
+    constant's own rounding is one of them more. Results below 2^-126 are off by
+    that of the subnormal steps of e (2^-149) times |v|, at most 2^-142."""
+    v = torch.linspace(-80, 80, N).bfloat16()
+    if act == "gelu_tanh":
+        v = torch.linspace(-9, 9, N).bfloat16()
+    x = torch.zeros((T, K), dtype=torch.bfloat16)
+    w = torch.zeros((N, K), dtype=torch.bfloat16)
+    p = torch.arange(T) % 4
+    x[torch.arange(T), torch.arange(T) % K] = torch.exp2(-p.float()).bfloat16()
+    w[:, :min(T, K)] = v[:, None]
+    out = torch.empty((T, N), device="cuda")
+    capi.moe_linear(capi.MOE_DT_BF16, x.cuda(), None, w.cuda(), None, None, capi.ACTS[act], None, out)
+    pre = x.double().sum(1, keepdim=True) * v.double()
+    if act == "silu":
+        ref = pre * torch.special.expit(pre)
+    elif act == "sigmoid":
+        ref = torch.special.expit(pre)
+    else:
+        ref = pre * torch.special.expit(2 * math.sqrt(2 / math.pi) * (pre + 0.044715 * pre ** 3))
+    rel = 2.0 ** -20
+    if act == "gelu_tanh":
+        rel = rel + 7 * 2.0 ** -24 * (2 * math.sqrt(2 / math.pi) * (pre + 0.044715 * pre ** 3)).abs()
+    err = (out.cpu().double() - ref).abs()
+    tol = rel * ref.abs() + 2.0 ** -142
+    assert torch.all(err <= tol), (err / tol).max()
+
+
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+@pytest.mark.parametrize("T", [4, 300])
+def test_linear_activations_tails_in_bf16(cuda_lib, act, T):
+    """bf16 results far down the left tail: the fast exponential's error, (4 + 1.2
+    |v|) 2^-23 or below 2^-16 here, is far below the store's half step 2^-8. The
+    fast division gives zero where its divisor 1 + exp(-v) passes 2^126, that is for
+    v < -87.3: what it drops there is below 88.8 / 2^126 < 2^-119."""
+    v = torch.linspace(-84, 20, 512).bfloat16()
+    x = torch.zeros((T, 64), dtype=torch.bfloat16)
+    x[:, 0] = 1.0
+    w = torch.zeros((512, 64), dtype=torch.bfloat16)
+    w[:, 0] = v
+    b = torch.full((512,), -4.5, device="cuda")
+    out = torch.empty((T, 512), dtype=torch.bfloat16, device="cuda")
+    capi.moe_linear(capi.MOE_DT_BF16, x.cuda(), None, w.cuda(), None, b, capi.ACTS[act], None, out)
+    pre = v.double() - 4.5
+    ref = torch.special.expit(pre) * (pre if act == "silu" else 1.0)
+    tol = (2.0 ** -8 + 2.0 ** -15) * ref.abs() + 2.0 ** -119
+    assert torch.all((out.cpu().double() - ref).abs() <= tol)
