@@ -120,12 +120,11 @@ __device__ __forceinline__ void apply_act(float (&v)[C], int act) {
 }
 
 __device__ __forceinline__ float load_typed(const void* p, int dt, size_t i) {
-  if (dt == 4) return __ldg(static_cast<const float*>(p) + i);
-  const unsigned short b = __ldg(static_cast<const unsigned short*>(p) + i);
+  if (dt == 4) return static_cast<const float*>(p)[i];
+  const unsigned short b = static_cast<const unsigned short*>(p)[i];
   return dt == 0 ? __bfloat162float(__ushort_as_bfloat16(b)) : __half2float(__ushort_as_half(b));
 }
 
-// The residual may be the output itself: no read-only load.
 __device__ __forceinline__ float load_residual(const void* p, int dt, size_t i) {
   if (dt == 4) return static_cast<const float*>(p)[i];
   if (dt == 0) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
@@ -244,7 +243,7 @@ struct SplitOut {
     if (g.x_scale) {
       float xs[C];
 #pragma unroll
-      for (int i = 0; i < C; ++i) xs[i] = __ldg(g.x_scale + min(t0 + i, t_end - 1));
+      for (int i = 0; i < C; ++i) xs[i] = g.x_scale[min(t0 + i, t_end - 1)];
 #pragma unroll
       for (int i = 0; i < C; ++i) v[i] = v[i] * xs[i] * ws;
     }
@@ -419,7 +418,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   bool ok = false;
   if (warp >= 3) {
     if (n < g.N) {  // fetched while the sum is still being built
-      if (g.x_scale) o.ws = __ldg(g.w_scale + static_cast<size_t>(n) * g.w_scale_step);
+      if (g.x_scale) o.ws = g.w_scale[static_cast<size_t>(n) * g.w_scale_step];
       if (g.bias) o.bias = load_typed(g.bias, g.bias_dt, n);
     }
     o.residual_of(res, c_lo, c_hi);
@@ -769,7 +768,7 @@ __device__ __forceinline__ void split_rows(const LinearArgs& g, uint32_t part, u
     float ws[4], bias[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      ws[i] = g.w_scale && i < cols ? __ldg(g.w_scale + static_cast<size_t>(n + i) * g.w_scale_step) : 1.f;
+      ws[i] = g.w_scale && i < cols ? g.w_scale[static_cast<size_t>(n + i) * g.w_scale_step] : 1.f;
       bias[i] = g.bias && i < cols ? load_typed(g.bias, g.bias_dt, n + i) : 0.f;
     }
     // two rows at a time: their remote loads are in flight together
@@ -780,7 +779,7 @@ __device__ __forceinline__ void split_rows(const LinearArgs& g, uint32_t part, u
       for (int j = 0; j < R; ++j) {
         const int t = t0 + r0 + j;
         const bool in = t < g.T;
-        xs[j] = g.x_scale && in ? __ldg(g.x_scale + t) : 1.f;
+        xs[j] = g.x_scale && in ? g.x_scale[t] : 1.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[j][i] = res[j][i] = 0.f;
         if (g.residual && in) load_res4(g, t * g.ldr + n, cols, res[j]);
@@ -1015,7 +1014,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tile_coords(g, tile, mt, nt);
       const int row0 = mt * 2 * kTileM + static_cast<int>(rank) * kTileM + 32 * q;
       const int t = row0 + lane;
-      const float xs = g.x_scale && t < g.T ? __ldg(g.x_scale + t) : 1.f;
+      const float xs = g.x_scale && t < g.T ? g.x_scale[t] : 1.f;
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
 
       // weight scale, bias and residual of chunk c, fetched a chunk ahead
@@ -1024,7 +1023,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       auto fetch = [&](int c) {
         const int n0 = nt * g.tn + 32 * c;
         const bool in = c < chunks && row0 < g.T && n0 + lane < g.N;
-        if (FP8) ws = in ? __ldg(g.w_scale + static_cast<size_t>(n0 + lane) * g.w_scale_step) : 1.f;
+        if (FP8) ws = in ? g.w_scale[static_cast<size_t>(n0 + lane) * g.w_scale_step] : 1.f;
         if (g.bias) bias = in ? load_typed(g.bias, g.bias_dt, n0 + lane) : 0.f;
         if (!PROMOTE && g.residual && c < chunks && row0 < g.T && n0 < g.N) fetch_residual<2, U>(g, res, row0, n0, lane);
       };

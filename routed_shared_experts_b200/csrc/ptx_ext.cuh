@@ -29,7 +29,9 @@ __device__ __forceinline__ bool elect_one() {
 // the kernels before this one have completed and their writes are visible. A
 // kernel launched with launch_early() (host) calls both before its first access
 // to global memory, so only what comes before them - the launch itself, barriers,
-// TMEM - overlaps its predecessor.
+// TMEM - overlaps its predecessor. Such a kernel loads its operands with plain
+// loads: the read-only path (ld.global.nc) is defined for memory that nothing
+// writes while the kernel runs, and the predecessor still does.
 __device__ __forceinline__ void grid_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -93,8 +93,8 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 }
 
 __device__ __forceinline__ float route_logit(const RouteArgs& a, size_t row, int e) {
-  if (a.dtype == 4) return __ldg(static_cast<const float*>(a.logits) + row + e);
-  const unsigned short b = __ldg(static_cast<const unsigned short*>(a.logits) + row + e);
+  if (a.dtype == 4) return static_cast<const float*>(a.logits)[row + e];
+  const unsigned short b = static_cast<const unsigned short*>(a.logits)[row + e];
   return a.dtype == 0 ? __bfloat162float(__ushort_as_bfloat16(b)) : __half2float(__ushort_as_half(b));
 }
 
@@ -125,11 +125,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
     const int e = lane + 32 * i;
     const bool in = e < a.E;
     l[i] = in ? route_logit(a, row, e) : NEG_INF;
-    on[i] = !(in && a.mask) || __ldg(a.mask + e) != 0;
-    bias[i] = in && a.bias ? __ldg(a.bias + e) : 0.f;
+    on[i] = !(in && a.mask) || a.mask[e] != 0;
+    bias[i] = in && a.bias ? a.bias[e] : 0.f;
   }
   const size_t out = static_cast<size_t>(t) * a.k + lane;
-  if (a.num_valid && t >= __ldg(a.num_valid)) {
+  if (a.num_valid && t >= *a.num_valid) {
     if (lane < a.k) {
       a.ids[out] = kNoExpert;
       a.wts[out] = 0.f;

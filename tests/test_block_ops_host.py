@@ -137,3 +137,16 @@ def test_binding_leaves_malformed_calls_alone(lib):
         assert b.linear("bf16", x, None, x, None, None, "relu", None, x, None) is None
     del o  # the loop's own reference to the last one
     assert [sys.getrefcount(v) for v in objs] == counts
+
+
+def test_kernels_that_start_early_use_no_read_only_loads():
+    """A kernel launched while its predecessor drains (launch_early) may read what
+    that one still writes: loads through the read-only path, which is defined for
+    data that stays as it is for the kernel's whole life, have no place in it."""
+    import os
+    import re
+    for name in ("linear.cuh", "route.cuh", "norm.cuh"):
+        src = re.sub(r"//[^\n]*", "", open(os.path.join(build.CSRC, name)).read())
+        assert "grid_dependency_wait()" in src
+        for word in ("__ldg", ".nc.", "__restrict__"):
+            assert word not in src, (name, word)

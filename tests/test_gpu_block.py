@@ -262,3 +262,63 @@ def test_block_gated_8_bit_layers(cuda_lib, case):
     else:
         assert torch.equal(layer.w2slots[:, cfg.top_k:], layer.gate.float()[:, None].expand(-1, layer.m))
     assert torch.equal(layer.topk_ids, plain.topk_ids) and not torch.equal(layer.out, plain.out)
+
+
+@pytest.mark.parametrize("T,H,A,E", [(1, 256, 512, 16), (32, 2048, 2048, 128), (64, 520, 96, 64), (200, 1024, 256, 32),
+                                     (1000, 768, 512, 256)])
+def test_chain_of_the_operators_captured_over_many_steps(cuda_lib, T, H, A, E):
+    """Projection with residual, norm to fp8, router product on the codes and
+    their scales, routing: twelve steps in one graph, every input and the number
+    of tokens changing from step to step in the same buffers, each kernel starting
+    while its predecessor drains. The same bits as one call at a time."""
+    steps, k = 12, 4
+    g = torch.Generator().manual_seed(T)
+    randn = lambda *s: torch.randn(s, generator=g).cuda()  # noqa: E731
+    attn_in, res_in = randn(steps, T, A).bfloat16(), randn(steps, T, H).bfloat16()
+    rows = -(-H // 16) * 16  # fp8 rows of a multiple of 16 bytes
+    w_o, w_r = (randn(H, A) * 0.05).bfloat16(), torch.randint(0, 120, (E, rows), generator=g, dtype=torch.uint8).cuda()[:, :H]
+    w_scale_in, bias_in = torch.rand((steps, E), generator=g).cuda() * 0.01, randn(steps, E)
+    valid_in = torch.randint(0, T + 1, (steps, 1), generator=g, dtype=torch.int32).cuda()
+    mask_in = (torch.rand((steps, E), generator=g) > 0.2).to(torch.uint8).cuda()
+    gamma_in = 1 + 0.1 * randn(steps, H)
+    buf = lambda t: torch.empty_like(t[0])  # noqa: E731
+    attn, res, w_scale, bias, valid, mask, gamma = map(buf, (attn_in, res_in, w_scale_in, bias_in, valid_in, mask_in, gamma_in))
+    codes = torch.zeros((T, rows), dtype=torch.uint8, device="cuda")
+    tight = codes if rows == H else torch.empty((T, H), dtype=torch.uint8, device="cuda")
+    scale, logits = torch.empty(T, device="cuda"), torch.empty((T, E), device="cuda")
+    ids, wts = torch.empty((T, k), dtype=torch.int32, device="cuda"), torch.empty((T, k), device="cuda")
+    outs = [[torch.empty((steps,) + tuple(t.shape), dtype=t.dtype, device="cuda") for t in (res, tight, scale, logits, ids, wts)]
+            for _ in range(2)]
+
+    def step(i, out, sync):
+        for dst, src in ((attn, attn_in), (res, res_in), (w_scale, w_scale_in), (bias, bias_in), (valid, valid_in),
+                         (mask, mask_in), (gamma, gamma_in)):
+            dst.copy_(src[i])
+        sync()
+        capi.moe_linear(capi.MOE_DT_BF16, attn, None, w_o, None, None, 0, res, res)
+        sync()
+        capi.moe_rmsnorm_quantize(capi.MOE_DT_FP8_E4M3, res, None, gamma, EPS, None, None, tight, scale)
+        sync()
+        if tight is not codes:
+            codes[:, :H].copy_(tight)
+        capi.moe_linear(capi.MOE_DT_FP8_E4M3, codes[:, :H], scale, w_r, w_scale, bias, 0, None, logits)
+        sync()
+        capi.moe_route(logits, bias, mask, valid, k, capi.MOE_SCORE_SIGMOID, 4, 3, capi.MOE_GROUP_TOP2, True, 1.5, ids, wts)
+        sync()
+        for dst, src in zip(out, (res, tight, scale, logits, ids, wts)):
+            dst[i].copy_(src)
+
+    for i in range(steps):
+        step(i, outs[0], torch.cuda.synchronize)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in range(steps):
+            step(i, outs[1], lambda: None)
+    for _ in range(3):
+        for o in outs[1]:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert capi.device_error() == 0
+        for a, b in zip(*outs):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
