@@ -173,6 +173,11 @@ __device__ __forceinline__ void load_stage(uint8_t* dst, const CUtensorMap* tm, 
   }
 }
 
+// Uses of accumulator `acc` (0 or 1) in `n` accumulations that take turns.
+__host__ __device__ constexpr int acc_uses(int n, int acc) { return (n + 1 - acc) / 2; }
+// Parity whose wait ends with the release that follows an accumulator's last use.
+__host__ __device__ constexpr uint32_t last_release_parity(int uses) { return static_cast<uint32_t>(uses - 1) & 1u; }
+
 // ------------------------------------------------------------ K split over a cluster
 
 constexpr int kSplitThreads = 224;  // weight producer, MMA, token producer, four epilogue warps
@@ -390,7 +395,7 @@ __global__ void __launch_bounds__(kSplitThreads)
             }
           }
         }
-        umma_commit(&empty[stage]);
+        if (ks + n_stages < s1) umma_commit(&empty[stage]);  // a release that no refill waits for is not sent
         if (++stage == n_stages) {
           stage = 0;
           phase ^= 1u;
@@ -931,6 +936,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       bool ok = true;
       int j = 0;  // accumulation counter: accumulator j % 2
       const uint16_t pair_mask = static_cast<uint16_t>(3u << leader);
+      // Stages still to come. A release that no refill waits for is not sent: it could reach the other CTA's
+      // barrier after that CTA's end, where a kernel that started early may have its own.
+      int64_t to_come = static_cast<int64_t>((total - unit0 + n_units - 1) / n_units) * ns;
       for (int tile = unit0; tile < total && ok; tile += n_units) {
         for (int kc = 0; kc < n_kc && ok; ++kc, ++j) {
           const int acc = j & 1;
@@ -958,7 +966,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
               }
             }
-            umma_commit_pair_multicast(&empty[stage], pair_mask);
+            if (--to_come >= n_stages) umma_commit_pair_multicast(&empty[stage], pair_mask);
             if (++stage == n_stages) {
               stage = 0;
               phase ^= 1u;
@@ -967,7 +975,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (ok) umma_commit_pair_multicast(&acc_full[acc], pair_mask);
         }
       }
-      if (!ok) {
+      if (ok) {
+        // the epilogue's last releases: rank 1's are remote arrivals that the relaxed cluster barrier does not order
+        if (!SPLIT) {
+          for (int acc = 0; acc < 2 && ok; ++acc) {
+            const int uses = acc_uses(j, acc);
+            if (uses > 0) ok = mbar_wait(&acc_empty[acc], last_release_parity(uses), abort_flag);
+          }
+        }
+      } else {
         umma_commit_pair(mapa_shared(smem_u32(drain), leader));
         drain_wait(drain, 0);
       }
@@ -1125,7 +1141,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_relaxed();  // no CTA leaves while its peer may still signal its barriers
+  cluster_sync_relaxed();  // no CTA leaves while its peer's roles still wait on or signal its barriers
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, L::kTmemCols);

@@ -374,3 +374,22 @@ def test_linear_activations_tails_in_bf16(cuda_lib, act, T):
     ref = torch.special.expit(pre) * (pre if act == "silu" else 1.0)
     tol = (2.0 ** -8 + 2.0 ** -15) * ref.abs() + 2.0 ** -119
     assert torch.all((out.cpu().double() - ref).abs() <= tol)
+
+
+@pytest.mark.parametrize("odt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,N,K", [(257, 640, 520), (300, 2815, 136), (384, 4400, 64), (2100, 1500, 264), (66, 256, 7168)])
+def test_linear_back_to_back(cuda_lib, T, N, K, odt):
+    """Launches that start while the one before them ends, rows of the last tile's
+    second half missing (its CTA then releases the accumulators last of all): forty
+    in a row on alternating operands, each result as the first time."""
+    g = torch.Generator().manual_seed(T + N)
+    xs = [torch.randint(-3, 4, (T, K), generator=g).to(torch.bfloat16).cuda() for _ in range(2)]
+    w = torch.randint(-3, 4, (N, K), generator=g).to(torch.bfloat16).cuda()
+    want = [(x.double() @ w.double().t()).to(DT[odt]) for x in xs]
+    outs = [torch.empty((T, N), dtype=DT[odt], device="cuda") for _ in range(40)]
+    for i, o in enumerate(outs):
+        capi.moe_linear(capi.MOE_DT_BF16, xs[i % 2], None, w, None, None, 0, None, o)
+    torch.cuda.synchronize()
+    assert capi.device_error() == 0
+    for i, o in enumerate(outs):
+        assert torch.equal(o, want[i % 2]), i

@@ -45,3 +45,44 @@ def test_chunk_bytes_up_to_the_largest_rows(tmp_path):
     assert res.returncode == 0, res.stderr
     run = subprocess.run([str(exe)], capture_output=True, text=True)
     assert run.returncode == 0, run.stdout
+
+
+TAIL = r"""
+#include "linear.cuh"
+#include <cstdio>
+
+// A phase barrier as a count of completed phases: a wait on parity p passes when the
+// current phase's parity is not p.
+static bool passes(int completed, unsigned p) { return (completed & 1u) != p; }
+
+int main() {
+  int bad = 0;
+  for (int n = 0; n < 50; ++n) {
+    int used[2] = {0, 0};
+    for (int j = 0; j < n; ++j) ++used[j & 1];
+    for (int acc = 0; acc < 2; ++acc) {
+      const int uses = moe::acc_uses(n, acc);
+      if (uses != used[acc]) ++bad;
+      if (uses == 0) continue;
+      // before an accumulator's use the MMA thread has seen all releases but the last
+      const unsigned p = moe::last_release_parity(uses);
+      if (passes(uses - 1, p) || !passes(uses, p)) ++bad;
+    }
+  }
+  printf("%d\n", bad);
+  return bad != 0;
+}
+"""
+
+
+def test_the_last_release_of_an_accumulator_is_waited_for(tmp_path):
+    """The pair kernel's MMA thread ends with a wait for the release after each
+    accumulator's last use: the wait must not pass on the release before it."""
+    src, exe = tmp_path / "tail.cu", tmp_path / "tail"
+    src.write_text(TAIL)
+    cmd = [build._nvcc(), "-O1", "-std=c++17", *build.ARCH, "-cudart", "static", "-I", build.INCLUDE, "-I", build.CSRC,
+           "-o", str(exe), str(src)]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr
+    run = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert run.returncode == 0, run.stdout
