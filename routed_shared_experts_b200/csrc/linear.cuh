@@ -273,19 +273,22 @@ struct SplitOut {
   }
   // Columns c0 .. c0 + C - 1 of the S partial tiles ([token column][128 outputs];
   // `part`: this thread's output of column 0), this CTA's own first, so that the
-  // peers' reads spread.
+  // peers' reads spread. Only what finish() uses is read: the relaxed cluster barrier
+  // that ends the kernel does not wait for a load whose value nothing waits for, and a
+  // peer could be gone before it arrives.
   template <int C>
   __device__ __forceinline__ void join(uint32_t part, int rank, int S, int c0, int c_hi,
                                        const float (&r)[B]) const {
     float v[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) v[i] = 0.f;
+    const bool in = n < g.N;
 #pragma unroll 2
     for (int p = 0; p < S; ++p) {
       const uint32_t peer = mapa_shared(part, static_cast<uint32_t>((rank + p) & (S - 1)));
 #pragma unroll
       for (int i = 0; i < C; ++i)
-        v[i] += ld_shared_cluster_f32_if(peer + static_cast<uint32_t>((c0 + i) * kTileM * 4), c0 + i < c_hi);
+        v[i] += ld_shared_cluster_f32_if(peer + static_cast<uint32_t>((c0 + i) * kTileM * 4), in && c0 + i < c_hi);
     }
     finish(v, r, c0, c_hi);
   }
@@ -711,12 +714,18 @@ __device__ __forceinline__ void tile_coords(const LinearArgs& g, int tile, int& 
 // unit u of row r at u ^ (r & 7).
 __device__ __forceinline__ int part_unit(int r, int u, int tn) { return r * (tn / 4) + (u ^ (r & 7)); }
 
-__device__ __forceinline__ float4 ld_shared_cluster_f32x4(uint32_t cluster_addr) {
+// Zeros where `on` is false.
+__device__ __forceinline__ float4 ld_shared_cluster_f32x4_if(uint32_t cluster_addr, bool on) {
   float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(cluster_addr)
-               : "memory");
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.f32 %0, 0f00000000;\n\tmov.f32 %1, 0f00000000;\n\t"
+      "mov.f32 %2, 0f00000000;\n\tmov.f32 %3, 0f00000000;\n\t"
+      "@p ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n\t}\n"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(cluster_addr), "r"(static_cast<int>(on))
+      : "memory");
   return v;
 }
 
@@ -794,7 +803,9 @@ __device__ __forceinline__ void split_rows(const LinearArgs& g, uint32_t part, u
         const uint32_t peer = mapa_shared(part, (ctarank + 2u * static_cast<uint32_t>(p)) & (2u * S - 1u));
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-          const float4 f = ld_shared_cluster_f32x4(peer + 16u * static_cast<uint32_t>(part_unit(r0 + j, u, g.tn)));
+          // rows past T are not read: no load may be in flight when a peer ends (as in SplitOut::join)
+          const float4 f = ld_shared_cluster_f32x4_if(
+              peer + 16u * static_cast<uint32_t>(part_unit(r0 + j, u, g.tn)), t0 + r0 + j < g.T);
           v[j][0] += f.x;
           v[j][1] += f.y;
           v[j][2] += f.z;

@@ -150,3 +150,16 @@ def test_kernels_that_start_early_use_no_read_only_loads():
         assert "grid_dependency_wait()" in src
         for word in ("__ldg", ".nc.", "__restrict__"):
             assert word not in src, (name, word)
+
+
+def test_remote_shared_memory_is_read_under_a_predicate():
+    """A read of a peer CTA's shared memory whose value nothing uses is not waited
+    for by the relaxed cluster barrier that ends moe_linear's kernels: each takes a
+    predicate, and the calls give the condition under which the value is used."""
+    import os
+    import re
+    src = re.sub(r"//[^\n]*", "", open(os.path.join(build.CSRC, "linear.cuh")).read())
+    loads = re.findall(r'"([^"]*)ld\.shared::cluster', src)
+    assert loads and all(head.startswith("@p ") for head in loads), loads
+    calls = re.findall(r"ld_shared_cluster_f32(?:x4)?_if\(\s*(peer[^;]*);", src)
+    assert len(calls) == 2 and "in && c0 + i < c_hi" in calls[0] and "t0 + r0 + j < g.T" in calls[1], calls

@@ -393,3 +393,21 @@ def test_linear_back_to_back(cuda_lib, T, N, K, odt):
     assert capi.device_error() == 0
     for i, o in enumerate(outs):
         assert torch.equal(o, want[i % 2]), i
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 140, 2048), (3, 8, 4096), (33, 200, 2048), (64, 1025, 7168), (66, 130, 7168),
+                                   (130, 250, 4104), (401, 97, 3600)])
+def test_linear_joins_of_partly_filled_tiles(cuda_lib, T, N, K):
+    """Warps and rows of a K split that have nothing to finish, in launches that
+    follow one another without a gap."""
+    g = torch.Generator().manual_seed(N)
+    x = torch.randint(-3, 4, (T, K), generator=g).to(torch.bfloat16).cuda()
+    w = torch.randint(-3, 4, (N, K), generator=g).to(torch.bfloat16).cuda()
+    want = x.double() @ w.double().t()
+    outs = [torch.empty((T, N), dtype=torch.bfloat16 if i % 2 else torch.float32, device="cuda") for i in range(40)]
+    for o in outs:
+        capi.moe_linear(capi.MOE_DT_BF16, x, None, w, None, None, 0, None, o)
+    torch.cuda.synchronize()
+    assert capi.device_error() == 0
+    for o in outs:
+        assert torch.equal(o, want.to(o.dtype))
