@@ -926,7 +926,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
       }
-      if (!ok) {
+      if (ok) {
+        // The releases that no refill waited for: one may not reach this CTA's barrier after its end, where a kernel
+        // that started early may have its own. (k_linear_split does not send them, 0.3 us better where a launch takes
+        // 5; here that test in the MMA loop cost 2 % at 3532 x 5641 x 1408, and these waits pass during the epilogue.)
+        for (int i = 0; i < n_stages && ok; ++i) {
+          ok = mbar_wait(&empty[stage], phase ^ 1u, abort_flag);
+          if (++stage == n_stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      } else {
         if (rank == 0) {
           for (int s = 0; s < n_stages; ++s)
             if ((pending >> s) & 1u) drain_wait(&full[s], (parity >> s) & 1u);
@@ -947,9 +958,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       bool ok = true;
       int j = 0;  // accumulation counter: accumulator j % 2
       const uint16_t pair_mask = static_cast<uint16_t>(3u << leader);
-      // Stages still to come. A release that no refill waits for is not sent: it could reach the other CTA's
-      // barrier after that CTA's end, where a kernel that started early may have its own.
-      int64_t to_come = static_cast<int64_t>((total - unit0 + n_units - 1) / n_units) * ns;
       for (int tile = unit0; tile < total && ok; tile += n_units) {
         for (int kc = 0; kc < n_kc && ok; ++kc, ++j) {
           const int acc = j & 1;
@@ -977,7 +985,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
               }
             }
-            if (--to_come >= n_stages) umma_commit_pair_multicast(&empty[stage], pair_mask);
+            umma_commit_pair_multicast(&empty[stage], pair_mask);
             if (++stage == n_stages) {
               stage = 0;
               phase ^= 1u;
