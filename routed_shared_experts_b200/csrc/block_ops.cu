@@ -92,7 +92,7 @@ struct LinearCall {
   moe::LinearArgs g;
 };
 
-template <int BN, bool FP8, bool F32>
+template <int BN, bool FP8, bool F32, bool PROMOTE>
 moe_status_t launch_linear_split(const LinearCall& c, int S, cudaStream_t s) {
   using L = moe::SplitCfg<BN>;
   CUtensorMap tw, twt, tx, txt;
@@ -100,7 +100,7 @@ moe_status_t launch_linear_split(const LinearCall& c, int S, cudaStream_t s) {
   if (r != MOE_OK) return r;
   r = make_linear_maps(&tx, &txt, c.dtype, c.x, c.g.T, c.K, c.ldx, BN);
   if (r != MOE_OK) return r;
-  auto kern = moe::k_linear_split<BN, FP8, F32>;
+  auto kern = moe::k_linear_split<BN, FP8, F32, PROMOTE>;
   static std::atomic<int> attr_set[64];
   r = set_smem_attr(kern, 227 * 1024, attr_set);
   if (r != MOE_OK) return r;
@@ -197,14 +197,14 @@ LinearPlan plan_linear(int T, int N, int nk, bool f32_out) {
     // Weights on the MMA's M side. The K split that still runs all CTAs at one
     // time streams the weights fastest (N = K = 2048, one token: 8.6, 7.2, 6.3
     // us for 1, 2, 4 CTAs per tile and 10.1 for 8, whose clusters no longer
-    // fit; N = K = 7168: 21.7, 19.4, 23.4). fp32 results cut K into pieces of
-    // at most 14 atoms, as far as 8 CTAs go.
+    // fit; N = K = 7168: 21.7, 19.4, 23.4). fp32 results give each CTA a piece of
+    // at most 14 atoms, as far as 8 CTAs go; past that a CTA takes several in turn.
     p.bn = T <= 16 ? 16 : T <= 32 ? 32 : 64;
     const int tiles = (N - 1) / moe::kTileM + 1;
     p.split = 1;
     for (int S = 2; S <= 8 && ns >= S; S *= 2) {
       const int fit = S == 8 ? num_sms() * 3 / 4 : num_sms();
-      const bool precise = f32_out && (ns + p.split - 1) / p.split > 7;
+      const bool precise = f32_out && (ns + p.split - 1) / p.split > moe::kSplitPieceStages;
       if (static_cast<int64_t>(tiles) * S <= fit || precise) p.split = S;
     }
     return p;
@@ -237,13 +237,22 @@ LinearPlan plan_linear(int T, int N, int nk, bool f32_out) {
   return p;
 }
 
+template <bool FP8, bool F32, bool PROMOTE>
+moe_status_t launch_linear_bn(const LinearCall& c, const LinearPlan& p, cudaStream_t s) {
+  if (p.bn == 16) return launch_linear_split<16, FP8, F32, PROMOTE>(c, p.split, s);
+  if (p.bn == 32) return launch_linear_split<32, FP8, F32, PROMOTE>(c, p.split, s);
+  return launch_linear_split<64, FP8, F32, PROMOTE>(c, p.split, s);
+}
+
 template <bool FP8, bool F32>
 moe_status_t launch_linear(LinearCall& c, cudaStream_t s) {
   const LinearPlan p = plan_linear(c.g.T, c.g.N, c.g.nk, F32);
   if (p.tn) return launch_linear_pairs<FP8, F32>(c, p, s);
-  if (p.bn == 16) return launch_linear_split<16, FP8, F32>(c, p.split, s);
-  if (p.bn == 32) return launch_linear_split<32, FP8, F32>(c, p.split, s);
-  return launch_linear_split<64, FP8, F32>(c, p.split, s);
+  if constexpr (F32) {  // a CTA's share of K above one piece
+    const int ns = (c.g.nk + moe::kLinAtoms - 1) / moe::kLinAtoms;
+    if ((ns + p.split - 1) / p.split > moe::kSplitPieceStages) return launch_linear_bn<FP8, true, true>(c, p, s);
+  }
+  return launch_linear_bn<FP8, F32, false>(c, p, s);
 }
 
 template <int VPL>

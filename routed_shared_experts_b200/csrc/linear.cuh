@@ -181,6 +181,7 @@ __host__ __device__ constexpr uint32_t last_release_parity(int uses) { return st
 // ------------------------------------------------------------ K split over a cluster
 
 constexpr int kSplitThreads = 224;  // weight producer, MMA, token producer, four epilogue warps
+constexpr int kSplitPieceStages = 7;  // 14 atoms: the longest accumulation of an fp32 result
 
 template <int BN>
 struct SplitCfg {
@@ -189,9 +190,10 @@ struct SplitCfg {
   static constexpr int kStageBytes = (kAtomW + kAtomX) * kLinAtoms;
   static constexpr int kMaxStages = 6;
   static constexpr int kStageOffset = 1024;  // after the barriers
-  static constexpr int kTmemCols = BN < 32 ? 32 : BN;
+  // TMEM columns: two accumulators with PROMOTE, so that two CTAs on an SM hold 256 of the 512 at most
+  __host__ __device__ static constexpr int tmem_cols(bool promote) { return promote ? 2 * BN : BN < 32 ? 32 : BN; }
   static_assert(kStageBytes % 1024 == 0, "stages start on 1024-byte swizzle boundaries");
-  static_assert((2 * kMaxStages + 2) * 8 + 8 <= kStageOffset, "barriers");
+  static_assert((2 * kMaxStages + 5) * 8 + 8 <= kStageOffset, "barriers");
   // as many stages as fit `bytes` of shared memory (one CTA per SM, or two)
   __host__ __device__ static constexpr int stages(int bytes) {
     const int fit = (bytes - 1024 - kStageOffset) / kStageBytes;  // less the alignment slack
@@ -294,7 +296,13 @@ struct SplitOut {
   }
 };
 
-template <int BN, bool FP8, bool F32>
+// PROMOTE: this CTA's share of K is cut into accumulations of kSplitPieceStages stages
+// that take turns on two TMEM accumulators; the epilogue threads add them in fp32
+// registers. For fp32 results whose K is longer than one such piece for each of
+// the 8 CTAs of a cluster (S is 8 then). Positive bf16 values, 64 tokens, K = 57344:
+// off by 1.7e-6 of the result, as at K = 7168, against 2.9e-5 in one accumulation per
+// CTA; 32 x 2048 x 16384 takes 22.0 us, 22.3 in one accumulation.
+template <int BN, bool FP8, bool F32, bool PROMOTE>
 __global__ void __launch_bounds__(kSplitThreads)
     k_linear_split(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWt,
                    const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXt,
@@ -306,8 +314,9 @@ __global__ void __launch_bounds__(kSplitThreads)
   uint8_t* stages = smem + L::kStageOffset;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);
   uint64_t* empty = full + L::kMaxStages;
-  uint64_t* done = empty + L::kMaxStages;
-  uint64_t* drain = done + 1;
+  uint64_t* acc_full = empty + L::kMaxStages;  // [2] with PROMOTE, else [1]
+  uint64_t* acc_empty = acc_full + 2;          // [2], PROMOTE only
+  uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -318,19 +327,24 @@ __global__ void __launch_bounds__(kSplitThreads)
   const int ns = (g.nk + kLinAtoms - 1) / kLinAtoms;  // stages along K; this CTA's are s0 .. s1 - 1
   const int s0 = static_cast<int>(static_cast<long long>(ns) * rank / S);
   const int s1 = static_cast<int>(static_cast<long long>(ns) * (rank + 1) / S);
+  // accumulations that the share is cut into
+  const int n_kc = PROMOTE ? (s1 - s0 + kSplitPieceStages - 1) / kSplitPieceStages : 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < n_stages; ++s) {
       mbar_init(&full[s], 2);  // each producer arms it with its own bytes
       mbar_init(&empty[s], 1);
     }
-    mbar_init(done, 1);
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&acc_full[a], 1);
+      mbar_init(&acc_empty[a], 4);  // the epilogue warps
+    }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, L::kTmemCols);
+    tmem_alloc(tmem_slot, L::tmem_cols(PROMOTE));
     tmem_relinquish();
   }
   tc_fence_before();
@@ -379,34 +393,44 @@ __global__ void __launch_bounds__(kSplitThreads)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int ks = s0; ks < s1; ++ks) {
-        ok = mbar_wait(&full[stage], phase, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        const int na = min(kLinAtoms, g.nk - ks * kLinAtoms);
-        const uint32_t a_addr = smem_u32(stages + stage * L::kStageBytes);
+      for (int kc = 0; kc < n_kc && ok; ++kc) {
+        const int acc = PROMOTE ? kc & 1 : 0;
+        if (PROMOTE) {
+          ok = mbar_wait(&acc_empty[acc], ((static_cast<uint32_t>(kc) >> 1) & 1u) ^ 1u, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+        const int s_lo = PROMOTE ? s0 + kc * kSplitPieceStages : s0;
+        const int s_hi = PROMOTE ? min(s1, s_lo + kSplitPieceStages) : s1;
+        for (int ks = s_lo; ks < s_hi; ++ks) {
+          ok = mbar_wait(&full[stage], phase, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const int na = min(kLinAtoms, g.nk - ks * kLinAtoms);
+          const uint32_t a_addr = smem_u32(stages + stage * L::kStageBytes);
 #pragma unroll
-        for (int a = 0; a < kLinAtoms; ++a) {
-          if (a < na) {
-            const uint64_t adesc = sw128_kmajor_desc(a_addr + a * L::kAtomW);
-            const uint64_t bdesc = sw128_kmajor_desc(a_addr + L::kAtomW * kLinAtoms + a * L::kAtomX);
+          for (int a = 0; a < kLinAtoms; ++a) {
+            if (a < na) {
+              const uint64_t adesc = sw128_kmajor_desc(a_addr + a * L::kAtomW);
+              const uint64_t bdesc = sw128_kmajor_desc(a_addr + L::kAtomW * kLinAtoms + a * L::kAtomX);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {  // 32 K-bytes per MMA: +2 in the (addr >> 4) field
-              const uint32_t accum = (ks != s0 || (a | kk) != 0) ? 1u : 0u;
-              if (FP8) umma_f8(tmem_base, adesc + 2 * kk, bdesc + 2 * kk, idesc, accum);
-              else umma_f16(tmem_base, adesc + 2 * kk, bdesc + 2 * kk, idesc, accum);
+              for (int kk = 0; kk < 4; ++kk) {  // 32 K-bytes per MMA: +2 in the (addr >> 4) field
+                const uint32_t accum = (ks != s_lo || (a | kk) != 0) ? 1u : 0u;
+                if (FP8) umma_f8(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, idesc, accum);
+                else umma_f16(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, idesc, accum);
+              }
             }
           }
+          if (ks + n_stages < s1) umma_commit(&empty[stage]);  // a release that no refill waits for is not sent
+          if (++stage == n_stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
-        if (ks + n_stages < s1) umma_commit(&empty[stage]);  // a release that no refill waits for is not sent
-        if (++stage == n_stages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        if (ok) umma_commit(&acc_full[acc]);
       }
-      if (ok) {
-        umma_commit(done);
-      } else {
+      if (!ok) {
         umma_commit(drain);
         drain_wait(drain, 0);
       }
@@ -430,12 +454,32 @@ __global__ void __launch_bounds__(kSplitThreads)
       if (g.bias) o.bias = load_typed(g.bias, g.bias_dt, n);
     }
     o.residual_of(res, c_lo, c_hi);
-    ok = mbar_wait(done, 0, abort_flag);
-    ok = __all_sync(0xffffffffu, ok);
-    tc_fence_after();
   }
   const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
-  if (S == 1) {
+  float sum[PROMOTE ? BN : 1];
+  if (warp >= 3) {
+    for (int kc = 0; kc < n_kc; ++kc) {
+      const int acc = kc & 1;
+      ok = mbar_wait(&acc_full[acc], (static_cast<uint32_t>(kc) >> 1) & 1u, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      if constexpr (PROMOTE) {
+#pragma unroll
+        for (int c0 = 0; c0 < BN; c0 += 16) {
+          float v[16];
+          tmem_ld16(t_row + static_cast<uint32_t>(acc * BN + c0), v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sum[c0 + i] = kc == 0 ? v[i] : sum[c0 + i] + v[i];
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[acc]);
+      }
+    }
+  }
+  if (!PROMOTE && S == 1) {
     if (ok) {
       for (int c0 = 0; c0 < nv; c0 += 16) {
         float v[16];
@@ -455,7 +499,10 @@ __global__ void __launch_bounds__(kSplitThreads)
   } else {
     // the stages are free: every copy has landed and every MMA has read them
     float* part = reinterpret_cast<float*>(stages);  // [token column][128 outputs]
-    if (ok) {
+    if (PROMOTE && ok) {
+#pragma unroll
+      for (int c = 0; c < BN; ++c) part[c * kTileM + rowi] = sum[PROMOTE ? c : 0];
+    } else if (ok) {
       for (int c0 = 0; c0 < nv; c0 += 16) {
         float v[16];
         tmem_ld16(t_row + static_cast<uint32_t>(c0), v);
@@ -484,7 +531,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, L::kTmemCols);
+    tmem_dealloc(tmem_base, L::tmem_cols(PROMOTE));
   }
 }
 

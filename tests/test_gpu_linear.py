@@ -411,3 +411,43 @@ def test_linear_joins_of_partly_filled_tiles(cuda_lib, T, N, K):
     assert capi.device_error() == 0
     for o in outs:
         assert torch.equal(o, want.to(o.dtype))
+
+
+@pytest.mark.parametrize("T,N,K,dt", [(1, 300, 16384, "bf16"), (20, 1000, 28672, "fp16"), (64, 256, 16384, "bf16"),
+                                      (64, 256, 57344, "bf16"), (5, 130, 32768, "fp8"), (33, 20000, 7168, "bf16"),
+                                      (64, 256, 32768, "fp8")])
+def test_linear_fp32_results_keep_precision_at_any_length(cuda_lib, T, N, K, dt):
+    """A piece of 14 atoms is the longest accumulation of an fp32 result whatever
+    K: eight of them are K = 7168 (fp8: 14336). With positive values nothing cancels
+    and every cut of the tensor core's additions goes one way, so a sum of pieces is
+    off by the mean of their relative errors, which is the same for two full pieces
+    of one distribution and less for a short one: the relative error at K is that
+    at eight pieces, half of it again for the draw, and the roundings of the sums of
+    pieces (2^-24 each, fifteen at most). Accumulations as long as K / 8 would make
+    it grow with K."""
+    g = torch.Generator(device="cuda").manual_seed(T + N)
+    short = 14336 if dt == "fp8" else 7168
+    L = max(K, short)
+    x = torch.rand((T, L), generator=g, device="cuda").to(DT[dt])
+    w = (torch.rand((N, L), generator=g, device="cuda") * 0.05).to(DT[dt])
+    xs, ws = (torch.ones(n, device="cuda") for n in (T, N)) if dt == "fp8" else (None, None)
+    out = torch.empty((T, N), device="cuda")
+
+    def error(k):
+        capi.moe_linear(capi.DTYPES[dt], x[:, :k], xs, w[:, :k], ws, None, 0, None, out)
+        ref = torch.zeros((T, N), dtype=torch.float64, device="cuda")
+        for i in range(0, k, 1024):  # in slices: w in 64 bits is eight times its size
+            ref += x[:, i:min(i + 1024, k)].double() @ w[:, i:min(i + 1024, k)].double().t()
+        return ((out.double() - ref).norm() / ref.norm()).item()
+
+    e, e0 = error(K), error(short)
+    assert e <= 1.5 * e0 + 15 * 2.0 ** -24, (e, e0)
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 300, 16384), (16, 128, 7304), (17, 96, 8200), (33, 130, 28680), (64, 256, 57344),
+                                   (2, 20000, 14352), (40, 1025, 14336)])
+@pytest.mark.parametrize("dt", ["bf16", "fp8"])
+def test_linear_exact_long_k_fp32(cuda_lib, T, N, K, dt):
+    """Whole numbers (sums below 2^24), so equality, where a CTA adds several pieces
+    of K: one, two, three and more, the last one short, bias and residual."""
+    _check(T, N, -(-K // 16) * 16, dt, "f32", ints=True, bias="f32", residual=True, pad=16 if T % 2 else 0)
