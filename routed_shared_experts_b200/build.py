@@ -1,5 +1,6 @@
 """Build ``libmoe_b200.so`` (sm_100a) in-tree with nvcc, and with gcc the Python
-binding ``_binding.so`` of its small operators.
+binding ``_binding`` of its small operators (named for this Python's ABI; without
+gcc or Python's headers it is left out, and the calls take the checked path).
 
     python -m routed_shared_experts_b200.build [--force] [--ptxas-info]
 
@@ -23,7 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libmoe_b200.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
-BINDING_PATH = os.path.join(PKG, "_binding.so")  # csrc/binding.c, the Python fast path of the small operators
+# csrc/binding.c, the Python fast path of the small operators; another Python builds its own beside it
+BINDING_PATH = os.path.join(PKG, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -50,16 +52,24 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(s) <= t for s in _sources())
 
 
-def build_binding(force: bool = False) -> str:
+def build_binding(force: bool = False) -> str | None:
+    """Path of the binding, or None where it cannot be built: the library does not
+    need it."""
+    untagged = os.path.join(PKG, "_binding.so")  # any Python would load it
+    if os.path.exists(untagged):
+        os.remove(untagged)
     src = os.path.join(CSRC, "binding.c")
     if not force and os.path.exists(BINDING_PATH) and os.path.getmtime(src) <= os.path.getmtime(BINDING_PATH):
         return BINDING_PATH
-    cmd = [shutil.which("gcc") or "cc", "-O2", "-fPIC", "-shared", "-Wall", "-I",
-           sysconfig.get_paths()["include"], "-o", BINDING_PATH, src]
-    res = subprocess.run(cmd, capture_output=True, text=True)
+    cc, include = shutil.which("gcc") or shutil.which("cc"), sysconfig.get_paths()["include"]
+    if cc is None or not os.path.exists(os.path.join(include, "Python.h")):
+        sys.stderr.write("no C compiler or no Python headers: the binding is not built, calls take the checked path\n")
+        return None
+    res = subprocess.run([cc, "-O2", "-fPIC", "-shared", "-Wall", "-I", include, "-o", BINDING_PATH, src],
+                         capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError(f"gcc failed ({res.returncode})")
+        raise RuntimeError(f"{cc} failed ({res.returncode})")
     return BINDING_PATH
 
 

@@ -107,3 +107,56 @@ def test_an_empty_tensor_is_not_an_absent_one(calls, call):
     with pytest.raises(ValueError):
         call(lambda dtype: T((0,), dtype))
     assert not calls
+
+
+def test_the_library_does_not_need_the_binding():
+    """Without a binding the library loads, and the operators' calls go through the
+    checked path: refused arguments come back as before, no rows are no error."""
+    import subprocess
+    import sys
+    code = """
+import sys
+sys.modules["routed_shared_experts_b200._binding"] = None  # its import raises
+import torch
+from routed_shared_experts_b200 import capi
+assert capi.sorted_capacity(32, 8, 128, 16) > 0
+capi._current_device, capi._current_stream = (lambda: 0), (lambda dev: 0)
+class T:
+    dtype, shape, device = torch.bfloat16, torch.Size((0, 64)), "cuda:0"
+    stride = lambda s: (64, 1)
+    get_device = lambda s: 0
+    data_ptr = lambda s: 0
+    numel = lambda s: 0
+    is_contiguous = lambda s: True
+class W(T):
+    shape = torch.Size((8, 64))
+    data_ptr = lambda s: 0x10000
+class O(T):
+    shape = torch.Size((0, 8))
+    stride = lambda s: (8, 1)
+capi.moe_linear(0, T(), None, W(), None, None, 0, None, O())
+try:
+    capi.moe_linear(0, T(), None, W(), None, None, 17, None, O())
+except capi.MoEError as e:
+    print("refused", e.status)
+"""
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=build.ROOT)
+    assert res.returncode == 0, res.stderr
+    assert res.stdout.split() == ["refused", "-1"]
+
+
+def test_the_binding_is_optional_and_of_one_abi(monkeypatch, tmp_path, capsys):
+    """Its file name carries Python's ABI, and neither a missing compiler nor
+    missing headers stop the build."""
+    import sysconfig
+    assert build.BINDING_PATH.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    assert ".cpython-" in build.BINDING_PATH
+    monkeypatch.setattr(build, "BINDING_PATH", str(tmp_path / "b.so"))
+    with monkeypatch.context() as m:
+        m.setattr(build.shutil, "which", lambda name: None)
+        assert build.build_binding(force=True) is None
+    with monkeypatch.context() as m:
+        m.setattr(build.sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+        assert build.build_binding(force=True) is None
+    assert "checked path" in capsys.readouterr().err and not (tmp_path / "b.so").exists()
+    assert build.build_binding() == str(tmp_path / "b.so")
