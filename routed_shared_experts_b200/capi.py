@@ -314,6 +314,13 @@ def _check_type(t, name, types):
         raise TypeError(f"{name} has type {t.dtype}")
 
 
+def _int(v, name):
+    """A number that the entry point takes in 32 bits (ctypes would cut it to them)."""
+    if not -(1 << 31) <= v < 1 << 31:
+        raise ValueError(f"{name} is {v}, past 32 bits")
+    return v
+
+
 def _vec(t, name, n, types):
     """Address of a dense tensor of n elements (None: NULL)."""
     if t is None:
@@ -357,8 +364,8 @@ def moe_linear(dtype, x, x_scale, w, w_scale, bias, act, residual, out, stream=N
             raise ValueError("w_scale has no elements")
     status = (_LIB or lib()).moe_linear(
         dtype, x.data_ptr(), ldx, _vec(x_scale, "x_scale", T, _F32), w.data_ptr(), ldw,
-        _vec(w_scale, "w_scale", ws_rows, _F32), ws_rows, pb, bias_dt, act, pr, ldr, out.data_ptr(),
-        _FLOAT_DT[out_type], ldo, T, N, K, _current_stream(dev) if stream is None else stream.cuda_stream)
+        _vec(w_scale, "w_scale", ws_rows, _F32), _int(ws_rows, "w_scale's length"), pb, bias_dt, _int(act, "act"), pr,
+        ldr, out.data_ptr(), _FLOAT_DT[out_type], ldo, _int(T, "T"), _int(N, "N"), _int(K, "K"), _current_stream(dev) if stream is None else stream.cuda_stream)
     if status:
         raise MoEError("moe_linear", status)
 
@@ -381,8 +388,9 @@ def moe_route(logits, bias, expert_mask, num_valid, top_k, score, n_group, topk_
     status = (_LIB or lib()).moe_route(
         logits.data_ptr(), _FLOAT_DT[logits.dtype], ld, bias if bias is None else _vec(bias, "bias", E, _F32),
         expert_mask if expert_mask is None else _vec(expert_mask, "expert_mask", E, _BYTES),
-        num_valid if num_valid is None else _vec(num_valid, "num_valid", 1, _I32), T, E, top_k, score, n_group,
-        topk_group, group_score, renormalize, routed_scaling_factor, _vec(topk_ids, "topk_ids", n, _I32),
+        num_valid if num_valid is None else _vec(num_valid, "num_valid", 1, _I32), _int(T, "T"), _int(E, "E"),
+        _int(top_k, "top_k"), _int(score, "score"), _int(n_group, "n_group"), _int(topk_group, "topk_group"),
+        _int(group_score, "group_score"), renormalize, routed_scaling_factor, _vec(topk_ids, "topk_ids", n, _I32),
         _vec(topk_weights, "topk_weights", n, _F32), _current_stream(dev) if stream is None else stream.cuda_stream)
     if status:
         raise MoEError("moe_route", status)
@@ -404,9 +412,10 @@ def moe_rmsnorm_quantize(quant, x, residual, gamma, eps, residual_out, y, codes,
     mx = quant == MOE_DT_MXFP8_E4M3
     dev = _device(x, gamma, y, residual, residual_out, codes, scale)
     status = (_LIB or lib()).moe_rmsnorm_quantize(
-        _FLOAT_DT.get(xt, MOE_DT_F32), MOE_DT_NONE if quant is None else quant, _vec(x, "x", n, same),
+        _FLOAT_DT.get(xt, MOE_DT_F32), MOE_DT_NONE if quant is None else _int(quant, "quant"), _vec(x, "x", n, same),
         residual if residual is None else _vec(residual, "residual", n, same),
-        _vec(gamma, "gamma", H, (xt, torch.float32)), _FLOAT_DT.get(gamma.dtype, MOE_DT_F32), eps, T, H,
+        _vec(gamma, "gamma", H, (xt, torch.float32)), _FLOAT_DT.get(gamma.dtype, MOE_DT_F32), eps, _int(T, "T"),
+        _int(H, "H"),
         residual_out if residual_out is None else _vec(residual_out, "residual_out", n, same),
         y if y is None else _vec(y, "y", n, same), codes if codes is None else _vec(codes, "codes", n, _CODES),
         scale if scale is None else _vec(scale, "scale", n // 32 if mx else T, (torch.uint8,) if mx else _F32),

@@ -122,8 +122,9 @@ static PyObject* not_plain(void) {
 }
 
 static int int_of(PyObject* o, int* v) {
-  *v = (int)PyLong_AsLong(o);
-  return !PyErr_Occurred();
+  const long l = PyLong_AsLong(o);
+  *v = (int)l;
+  return !PyErr_Occurred() && l == *v;
 }
 
 static int is_float(int type) { return type == BF16 || type == FP16 || type == F32; }
@@ -149,7 +150,7 @@ static PyObject* py_linear(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   const int w_ok = dtype == E4M3 ? (w.type == U8 || w.type == E4M3) : w.type == dtype;
   if ((dtype != BF16 && dtype != FP16 && dtype != E4M3) || x.type != want || !w_ok || !is_float(o.type) ||
       w.cols != x.cols || o.rows != x.rows || o.cols != w.rows || (xs.ptr && (xs.type != F32 || xs.rows != x.rows)) ||
-      (ws.ptr && ws.type != F32) || (b.ptr && (!is_float(b.type) || b.rows != w.rows)))
+      (ws.ptr && (ws.type != F32 || ws.rows > INT32_MAX)) || (b.ptr && (!is_float(b.type) || b.rows != w.rows)))
     return not_plain();
   int status;
   Py_BEGIN_ALLOW_THREADS

@@ -160,3 +160,32 @@ def test_the_binding_is_optional_and_of_one_abi(monkeypatch, tmp_path, capsys):
         assert build.build_binding(force=True) is None
     assert "checked path" in capsys.readouterr().err and not (tmp_path / "b.so").exists()
     assert build.build_binding() == str(tmp_path / "b.so")
+
+
+@pytest.mark.parametrize("call", [
+    lambda: _route(k=2 + (1 << 32)), lambda: _route(score=1 << 32), lambda: _route(n_group=1 + (1 << 32)),
+    lambda: _route(topk_group=1 - (1 << 32)), lambda: _route(gs=1 << 33), lambda: _linear(act=1 << 32),
+    lambda: _linear(act=(1 << 32) + 2), lambda: _norm(quant=(1 << 32) - 1, y=T((4, 64), BF)),
+    lambda: _norm(quant=1 << 70, y=T((4, 64), BF)), lambda: _linear(act=-(1 << 64)),
+    lambda: _linear(dtype=capi.MOE_DT_FP8_E4M3, xs=T((4,), F32), ws=T(((1 << 32) + 1,), F32)),
+])
+def test_numbers_past_32_bits_are_refused(calls, call):
+    """Not taken for their low 32 bits, which may well be valid."""
+    with pytest.raises(ValueError):
+        call()
+    assert not calls
+
+
+@pytest.mark.parametrize("rows", [1 << 31, (1 << 32) + 4])
+def test_rows_past_32_bits_are_refused(calls, rows):
+    """2^32 + 4 rows of 16 bits fit a GPU; a call on 4 of them is not the one that
+    was made."""
+    with pytest.raises(ValueError):
+        capi.moe_route(T((rows, 1), BF), None, None, None, 1, 0, 1, 1, 0, True, 1.0, T((rows, 1), I32), T((rows, 1), F32))
+    with pytest.raises(ValueError):
+        capi.moe_rmsnorm_quantize(None, T((rows, 8), BF), None, T((8,), BF), 1e-6, None, T((rows, 8), BF), None, None)
+    with pytest.raises(ValueError):
+        capi.moe_linear(capi.MOE_DT_BF16, T((rows, 8), BF), None, T((4, 8), BF), None, None, 0, None, T((rows, 4), BF))
+    with pytest.raises(ValueError):
+        capi.moe_linear(capi.MOE_DT_BF16, T((4, 8), BF), None, T((rows, 8), BF), None, None, 0, None, T((4, rows), BF))
+    assert not calls
