@@ -89,6 +89,10 @@ def lib() -> ctypes.CDLL:
     return _LIB
 
 
+# None in a torch built without CUDA, which has no tensors that a call could take
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
 _BINDING = None  # csrc/binding.c: well-formed calls of the small operators without ctypes
 
 
@@ -108,12 +112,14 @@ def _load_binding(handle):
     try:
         from . import _binding
     except ImportError:
+        _binding = None
+    if _binding is None or _current_device is None:
         _BINDING = _CheckedPath
         return
     address = lambda name: ctypes.cast(getattr(handle, name), ctypes.c_void_p).value  # noqa: E731
     _binding.init((address("moe_linear"), address("moe_route"), address("moe_rmsnorm_quantize")),
                   (torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn, torch.uint8, torch.bool,
-                   torch.int32), torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+                   torch.int32), _current_device, _current_stream)
     _BINDING = _binding
 
 
@@ -260,8 +266,6 @@ _OPERAND_DT = {MOE_DT_BF16: (torch.bfloat16,), MOE_DT_FP16: (torch.float16,),
                MOE_DT_FP8_E4M3: (torch.uint8, torch.float8_e4m3fn)}
 _F32, _I32, _BYTES = (torch.float32,), (torch.int32,), (torch.uint8, torch.bool)
 _CODES = (torch.uint8, torch.float8_e4m3fn)
-
-_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 # The wrappers below are called once per operator of a decode step, whose kernels
 # take a few microseconds. The binding makes a well-formed call (None: it is not

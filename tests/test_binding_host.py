@@ -65,8 +65,9 @@ def calls(request, monkeypatch):
     monkeypatch.setattr(capi, "_current_device", lambda: 0)
     monkeypatch.setattr(capi, "_current_stream", lambda dev: 0)
     yield seen
+    monkeypatch.undo()
     if request.param == "binding":
-        capi._load_binding(real)
+        capi._load_binding(real)  # its own functions again
 
 
 def _linear(x=None, xs=None, ws=None, b=None, r=None, dtype=capi.MOE_DT_BF16, act=0):
@@ -189,3 +190,23 @@ def test_rows_past_32_bits_are_refused(calls, rows):
     with pytest.raises(ValueError):
         capi.moe_linear(capi.MOE_DT_BF16, T((4, 8), BF), None, T((rows, 8), BF), None, None, 0, None, T((4, rows), BF))
     assert not calls
+
+
+def test_import_with_a_torch_built_without_cuda():
+    """The size queries and refusals of capi need no CUDA in torch."""
+    import subprocess
+    import sys
+    code = """
+import torch
+del torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+from routed_shared_experts_b200 import capi
+assert capi.sorted_capacity(32, 8, 128, 16) > 0
+x = torch.zeros((4, 64), dtype=torch.bfloat16)
+try:
+    capi.moe_linear(capi.MOE_DT_BF16, x, None, x, None, None, 0, None, torch.zeros((4, 4), dtype=torch.bfloat16))
+except ValueError:
+    print("refused")
+"""
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=build.ROOT)
+    assert res.returncode == 0, res.stderr
+    assert res.stdout.split() == ["refused"]
