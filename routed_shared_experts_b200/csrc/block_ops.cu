@@ -43,6 +43,19 @@ moe_status_t launch_early(void (*kern)(P...), unsigned grid, unsigned threads, s
   return MOE_OK;
 }
 
+// make_map in a thread that may not have used CUDA before: the driver call behind it
+// needs the device's context to be current, which a thread gets from its first
+// runtime call that uses the device. One retry, so that other calls pay nothing.
+moe_status_t make_map_any_thread(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* base,
+                                 const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+  const moe_status_t r = make_map(m, dt, rank, base, dims, strides, box);
+  if (r == MOE_OK) return r;
+  int dev = 0;
+  MOE_CK(cudaGetDevice(&dev));
+  MOE_CK(cudaSetDevice(dev));
+  return make_map(m, dt, rank, base, dims, strides, box);
+}
+
 // An operand of the linear product, `rows` rows of K elements, ld elements
 // apart: `m` as [atoms][rows][128 bytes] over the K atoms that K fills, read
 // kLinAtoms atoms x box_rows rows at a time, and `tail` as the plain matrix,
@@ -62,14 +75,14 @@ moe_status_t make_linear_maps(CUtensorMap* m, CUtensorMap* tail, int dtype, cons
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
     const cuuint64_t st[1] = {row};
     const cuuint32_t box[2] = {ke, static_cast<cuuint32_t>(box_rows)};
-    const moe_status_t r = make_map(tail, dt, 2, base, dims, st, box);
+    const moe_status_t r = make_map_any_thread(tail, dt, 2, base, dims, st, box);
     if (r != MOE_OK) return r;
   }
   if (whole) {
     const cuuint64_t dims[3] = {ke, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(K / ke)};
     const cuuint64_t st[2] = {row, moe::kTileKBytes};
     const cuuint32_t box[3] = {ke, static_cast<cuuint32_t>(box_rows), moe::kLinAtoms};
-    const moe_status_t r = make_map(m, dt, 3, base, dims, st, box);
+    const moe_status_t r = make_map_any_thread(m, dt, 3, base, dims, st, box);
     if (r != MOE_OK) return r;
   }
   if (!ragged) *tail = *m;

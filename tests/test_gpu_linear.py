@@ -451,3 +451,58 @@ def test_linear_exact_long_k_fp32(cuda_lib, T, N, K, dt):
     """Whole numbers (sums below 2^24), so equality, where a CTA adds several pieces
     of K: one, two, three and more, the last one short, bias and residual."""
     _check(T, N, -(-K // 16) * 16, dt, "f32", ints=True, bias="f32", residual=True, pad=16 if T % 2 else 0)
+
+
+def test_linear_from_two_threads(cuda_lib):
+    """Calls of two Python threads on streams of their own (the binding lets the
+    other thread run during the launch)."""
+    import threading
+    g = torch.Generator().manual_seed(2)
+    w = torch.randint(-3, 4, (640, 512), generator=g).to(torch.bfloat16).cuda()
+    xs = [torch.randint(-3, 4, (t, 512), generator=g).to(torch.bfloat16).cuda() for t in (3, 300)]
+    want = [(x.double() @ w.double().t()).float() for x in xs]
+    outs = [[torch.zeros((x.shape[0], 640), device="cuda") for _ in range(50)] for x in xs]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for o in outs[i]:
+                    capi.moe_linear(capi.MOE_DT_BF16, xs[i], None, w, None, None, 0, None, o)
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for i in range(2):
+        for o in outs[i]:
+            assert torch.equal(o, want[i])
+
+
+def test_first_call_of_a_thread(cuda_lib):
+    """A thread whose first use of CUDA is this call: no context is current yet."""
+    import threading
+    x = torch.ones((4, 64), dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros((4, 4), device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    failed = []
+
+    def work():
+        try:
+            capi.moe_linear(capi.MOE_DT_BF16, x, None, x, None, None, 0, None, out, s)
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    s.synchronize()
+    assert not failed and torch.all(out == 64)
