@@ -453,6 +453,57 @@ def test_linear_exact_long_k_fp32(cuda_lib, T, N, K, dt):
     _check(T, N, -(-K // 16) * 16, dt, "f32", ints=True, bias="f32", residual=True, pad=16 if T % 2 else 0)
 
 
+@pytest.mark.parametrize("T", [1, 5, 70, 300])
+@pytest.mark.parametrize("N,K", [(1, 1), (2, 3), (3, 7), (1, 9), (130, 1), (33, 63), (7, 65), (5, 127), (3, 129)])
+def test_linear_smallest_and_odd_k(cuda_lib, T, N, K):
+    """K of any length, in rows whose stride is a multiple of 16 bytes; what lies
+    between K and the next row (NaN here) is not read as part of the sum."""
+    g = torch.Generator().manual_seed(T + 10 * N + K)
+    for dt, odt in (("bf16", "f32"), ("fp16", "fp16"), ("fp8", "bf16")):
+        ld = -(-K // 16) * 16 + 16
+        xb, wb = (torch.full((n, ld), float("nan")).to(DT[dt]).cuda() for n in (T, N))
+        x, w = (torch.randint(-3, 4, (n, K), generator=g).float() for n in (T, N))
+        xb[:, :K], wb[:, :K] = x.to(DT[dt]).cuda(), w.to(DT[dt]).cuda()
+        s = [torch.ones(n, device="cuda") for n in (T, N)] if dt == "fp8" else (None, None)
+        out = torch.empty((T, N), dtype=DT[odt], device="cuda")
+        capi.moe_linear(capi.DTYPES[dt], xb[:, :K], s[0], wb[:, :K], s[1], None, 0, None, out)
+        torch.cuda.synchronize()
+        assert capi.device_error() == 0
+        assert torch.equal(out.cpu(), (x.double() @ w.double().t()).to(DT[odt])), (dt, odt)
+
+
+def test_first_calls_of_a_process_inside_a_capture(cuda_lib):
+    """A process whose first call of each operator is a captured one, every kernel
+    choice of the product among them."""
+    import subprocess
+    import sys
+    from routed_shared_experts_b200 import build
+    code = """
+import torch
+from routed_shared_experts_b200 import capi
+w = torch.ones((512, 4096), dtype=torch.bfloat16, device="cuda")
+xs = [torch.ones((t, 4096), dtype=torch.bfloat16, device="cuda") for t in (1, 40, 100, 500, 3000)]
+outs = [torch.zeros((x.shape[0], 512), dtype=d, device="cuda") for x in xs for d in (torch.bfloat16, torch.float32)]
+ids, wt = torch.zeros((500, 4), dtype=torch.int32, device="cuda"), torch.zeros((500, 4), device="cuda")
+gamma, y = torch.ones(512, device="cuda"), torch.zeros((500, 512), dtype=torch.bfloat16, device="cuda")
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    for i, o in enumerate(outs):
+        capi.moe_linear(capi.MOE_DT_BF16, xs[i // 2], None, w, None, None, 0, None, o)
+    capi.moe_rmsnorm_quantize(None, outs[6], None, gamma, 1e-6, None, y, None, None)
+    capi.moe_route(outs[7], None, None, None, 4, 0, 8, 2, 0, True, 1.0, ids, wt)
+for _ in range(2):
+    g.replay()
+torch.cuda.synchronize()
+assert capi.device_error() == 0
+assert all(torch.all(o == 4096) for o in outs)
+assert torch.all(y == 1) and torch.all(ids == torch.arange(4, device="cuda")) and torch.all(wt == 0.25)
+print("ok")
+"""
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=build.ROOT)
+    assert res.returncode == 0 and res.stdout.strip() == "ok", res.stderr
+
+
 def test_linear_from_two_threads(cuda_lib):
     """Calls of two Python threads on streams of their own (the binding lets the
     other thread run during the launch)."""

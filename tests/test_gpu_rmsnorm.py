@@ -280,3 +280,42 @@ def test_norm_fp8_codes_are_of_the_ieee_quotient(cuda_lib, H):
 
 
 _E4M3 = sorted({float(v) for v in torch.arange(0, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).float()})
+
+
+def test_norm_mxfp8_infinities_and_nan(cuda_lib):
+    """A NaN spoils its own row; an infinity gives zeros beside it in the whole
+    row and NaN in its place. A block's exponent goes by its values that are not
+    NaN: those are zeros here, so its byte is 0."""
+    T, H = 4, 256
+    x, _, gamma = _inputs(T, H, "bf16", seed=1)
+    x[0, 3], x[1, 200] = float("nan"), float("-inf")
+    y = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+    c, s = torch.empty((T, H), dtype=torch.uint8, device="cuda"), torch.empty((T, H // 32), dtype=torch.uint8, device="cuda")
+    capi.moe_rmsnorm_quantize(QUANT["mxfp8"], x.cuda(), None, gamma.cuda(), 1e-6, None, y, c, s)
+    torch.cuda.synchronize()
+    y, c, s = y.cpu().float(), c.cpu().view(torch.float8_e4m3fn).float(), s.cpu()
+    assert torch.isnan(y[0]).all() and torch.isnan(c[0]).all() and torch.all(s[0] == 0)
+    assert torch.isnan(y[1, 200]) and torch.isnan(c[1, 200]) and torch.all(s[1] == 0)
+    keep = torch.arange(H) != 200
+    assert torch.all(y[1][keep] == 0) and torch.all(c[1][keep] == 0)
+    assert torch.isfinite(y[2:]).all() and torch.isfinite(c[2:]).all()
+
+
+def test_norm_mxfp8_gamma_infinities(cuda_lib):
+    """An infinite y that no infinite row made (an infinite gamma): its block
+    takes the largest exponent, 128 - 8, the infinity the largest code and its
+    finite neighbours vanish; other blocks do not notice."""
+    gamma = torch.linspace(-3, 3, 128, device="cuda")
+    gamma[40], gamma[50] = float("inf"), float("nan")
+    codes, scale = _norm_of_gamma(gamma, "mxfp8")
+    c, s = codes[0].cpu().view(torch.float8_e4m3fn).float(), scale[0].cpu()
+    assert c[40] == 448 and torch.isnan(c[50]) and s[1] == 127 + 120
+    rest = torch.arange(32, 64)
+    rest = rest[(rest != 40) & (rest != 50)]
+    assert torch.all(c[rest] == 0)
+    b = gamma.cpu().double().view(4, 32)
+    for i in (0, 2, 3):
+        e = math.floor(math.log2(b[i].abs().max())) - 8
+        assert s[i] == e + 127
+        want = (b[i] / 2.0 ** e).float().to(torch.float8_e4m3fn).float()
+        assert torch.equal(c[32 * i:32 * i + 32], want)
