@@ -271,7 +271,7 @@ moe_status_t launch_linear(LinearCall& c, cudaStream_t s) {
 template <int VPL>
 moe_status_t launch_route(const moe::RouteArgs& a, bool softmax, cudaStream_t s) {
   const size_t smem = a.n_group > 1 ? moe::kRouteWarps * a.groups.words(a.n_group) * sizeof(float) : 0;
-  const int blocks = (a.T + moe::kRouteWarps - 1) / moe::kRouteWarps;
+  const int blocks = (a.T - 1) / moe::kRouteWarps + 1;  // T goes up to 2^31 - 1
   // a grid that fills the SMs gains nothing from a successor's waiting blocks (4096 tokens: 12.2 against 13.0 us)
   return launch_early(softmax ? moe::k_route<VPL, true> : moe::k_route<VPL, false>, blocks, moe::kRouteWarps * 32, smem,
                       0, blocks <= 2 * num_sms(), s, a);

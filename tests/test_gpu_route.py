@@ -281,3 +281,15 @@ def test_route_live_group_below_the_fp32_range(cuda_lib, score):
         got = ids.cpu() // 8
         assert set(got.unique().tolist()) == set(others + [alive])
         assert torch.all(w > 0)  # all twenty picks live
+
+
+def test_route_most_rows_there_are(cuda_lib):
+    """T = 2^31 - 1, the largest that the call takes."""
+    T = (1 << 31) - 1
+    logits = torch.zeros((T, 1), dtype=torch.bfloat16, device="cuda")
+    ids = torch.full((T, 1), 7, dtype=torch.int32, device="cuda")
+    w = torch.zeros((T, 1), device="cuda")
+    capi.moe_route(logits, None, None, None, 1, 0, 1, 1, 0, True, 1.0, ids, w)
+    torch.cuda.synchronize()
+    for lo in range(0, T, 1 << 28):
+        assert torch.all(ids[lo:lo + (1 << 28)] == 0) and torch.all(w[lo:lo + (1 << 28)] == 1)
