@@ -471,6 +471,10 @@ moe_status_t shared_expert_gate_dot(int dtype, const void* x, const void* w, int
  *              between the rows is written.
  * No workspace; results do not depend on the launch (a K split is added in a
  * fixed order), but sums of different T, N or K may be ordered differently.
+ * The tensor core's additions cut where fp32 arithmetic rounds: over L products
+ * of one sign they are off by 2e-9 L (bf16) to 6e-9 L (fp16) of the sum, measured.
+ * fp32 results add pieces of at most 14 128-byte steps of K (896 values of 16
+ * bits) in fp32; a 16-bit result keeps one accumulation for the K of a CTA.
  * Checks: T >= 0 (T == 0: nothing is launched), N, K >= 1, none above 2^30,
  * ldx, ldw >= K, ldo, ldr >= N, none above 2^36; x and w 16-byte aligned with row strides of a multiple of 16
  * bytes (MOE_ERR_ALIGNMENT), out, residual, bias and the scales aligned to
@@ -499,7 +503,10 @@ moe_status_t moe_linear(int dtype, const void* x, int64_t ldx, const float* x_sc
  *   An expert is dead for a token when it is switched off, its logit is NaN or
  *   -inf, or its c is NaN or -inf. Dead experts of the kept groups are picked
  *   after all live ones, lowest index first, with weight 0; a row without a
- *   live expert gets weights 0. Logits of +inf share a softmax evenly.
+ *   live expert gets weights 0. Their slots run like any other and add 0 times
+ *   the expert's output: keep the weights of an expert that is switched off
+ *   finite where a row may be left with fewer live experts than top_k. Logits
+ *   of +inf share a softmax evenly.
  *   topk_ids     int32 [T,top_k], best first; topk_weights fp32 [T,top_k].
  * Against moe_router_topk: a bias, groups and either score in any combination,
  * 16-bit and strided logits, masks and padded batches; softmax is chosen by

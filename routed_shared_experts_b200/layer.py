@@ -26,7 +26,8 @@ class Routing:
     either score with a balance bias, groups, experts switched off and padded
     batches (``num_valid``: int32 [1] on the device; the rows behind it take no
     expert and keep what ``layer.out`` held). The tensors are read at every
-    forward, captured graphs included."""
+    forward, captured graphs included. A row left with fewer live experts than
+    top_k runs switched-off ones with weight 0: their weights have to be finite."""
     score: str = "softmax"             # 'softmax' | 'sigmoid'
     n_group: int = 1
     topk_group: int = 1
