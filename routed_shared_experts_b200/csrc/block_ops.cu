@@ -287,10 +287,10 @@ moe_status_t launch_rmsnorm(const moe::NormArgs& a, cudaStream_t s) {
 // Threads per row and 16-byte chunks per thread, by the row's chunk count: one
 // chunk per thread is the quickest row. Rows of 2049 to 4096 columns are cheaper
 // with four chunks per thread when there are enough of them to fill the SMs
-// (T = 4096: fp8 25.1 against 30.5 us, plain 22.3 against 22.6; T = 300: 4.9
-// against 4.9), and the two reductions of a wide fp8 row with half the warps
-// (H = 7168, T = 4096: 46.4 against 59.9 us, T = 32: 3.0 against 3.0; MXFP8,
-// with one, 49.0 against 46.3).
+// (T = 4096: fp8 24.6 against 30.6 us, MXFP8 24.5 against 25.4, plain 21.8 against
+// 25.0; T = 300: fp8 3.4 against 3.9 the other way round), and the two reductions
+// of a wide fp8 row with half the warps (H = 7168, T = 4096: 46.9 against 61.1 us,
+// T = 32: 2.6 against 2.8; MXFP8, with one, 42.4 against 41.7).
 template <typename TX, int Q>
 moe_status_t launch_rmsnorm_row(const moe::NormArgs& a, cudaStream_t s) {
   const int nc = a.H / 8;

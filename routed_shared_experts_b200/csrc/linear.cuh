@@ -27,8 +27,8 @@
 // What bounds it: with few tokens the weights' stream from HBM, N * K * size
 // bytes, which needs all SMs pulling at once; the K split is what supplies them
 // when N / 128 tiles are fewer than the SMs (32 tokens, 7168 x 7168 with
-// residual: 19.5 us, 5.3 TB/s, 83 % of the measured copy rate; the library's
-// product alone 25.9). Below about 10 MB of weights it is bound by latency: 4.6
+// residual: 19.8 us, 5.3 TB/s, 81 % of the measured copy rate; the library's
+// product alone 25.9). Below about 10 MB of weights it is bound by latency: 4.4
 // us for one token against 2048 x 2048.
 #pragma once
 #include <type_traits>
@@ -547,10 +547,12 @@ __global__ void __launch_bounds__(kSplitThreads)
 // residual reads and result writes are whole 64-byte row segments and no barrier
 // between warps is needed.
 //
-// What bounds it: at tn = 256 the MMAs (a stage of two atoms takes 1023 of the
-// ideal 1024 clocks), under the 1 kW power cap at T = 4096, N = K = 7168 (292 us
-// with residual, the library's product alone 306; 1.44 PFLOP/s against 1.38
-// sustained measured). Narrow tiles wait for their copies, whose round trip of
+// What bounds it: wide tiles by the MMAs (at tn = 256 a stage of two atoms takes
+// 1023 of the ideal 1024 clocks; T = 4096, N = K = 7168 runs at 224 outputs, tensor
+// pipe 89 % busy) and, kept up, by the 1 kW power cap: that product with residual
+// takes 306 us from a cool start and 348 sustained at 1.2 GHz, 1.21 PFLOP/s against
+// 1.38 measured sustained (the library's product alone, in turn with it: 314 and
+// 360). Narrow tiles wait for their copies, whose round trip of
 // about 1.45 us the stages that fit have to cover: hence as many as fit. Small
 // shapes are bound by what a launch, the first copy and the last tile's epilogue
 // take, 5 to 7 us.

@@ -12,8 +12,9 @@
 // once; a row stays in registers between the sum and the stores. TPR threads
 // share a row, V 16-byte chunks (8 values) each; narrow rows are packed several
 // to a block of 256 threads so that a block always has 256 threads' loads in
-// flight. Measured at 4096 x 7168 with residual, 16-bit rows and MXFP8 codes: 46.1
-// us for 265 MB, 5.7 TB/s; a device copy of as many bytes takes 47.3 us.
+// flight. Measured at 4096 x 7168 with residual, 16-bit rows and MXFP8 codes: 41.1 to
+// 41.6 us for 265 MB, 6.4 TB/s, the measured copy rate; to fp8 codes 46.6, two
+// reductions.
 #pragma once
 #include "ptx_ext.cuh"
 #include "quant.cuh"
@@ -112,9 +113,10 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) k_rmsnorm(const NormArg
 
   // 16-bit gamma is fetched with the row, or, where four chunks per thread leave few
   // registers, while the sum is reduced (4096 x 7168 fp8: 46.9 against 51.3 us; 1792 x
-  // 16384 MXFP8: 44.0 against 45.0). Early is better elsewhere (4096 x 7168 MXFP8 42.0
-  // against 46.4, 4096 x 4096 fp8 24.5 against 27.4, 1792 x 16384 fp8 49.9 against 61.5).
-  constexpr bool kGammaLate = V == 4 && TPR == (Q == kNormFp8 ? 256 : 512);
+  // 16384 MXFP8: 44.0 against 45.0; 4096 x 4096 plain: 21.8 against 23.0). Early is
+  // better elsewhere (4096 x 7168 MXFP8 42.0 against 46.4; 4096 x 4096 fp8 24.5 against
+  // 27.4, MXFP8 24.5 against 25.5; 1792 x 16384 fp8 49.9 against 61.5).
+  constexpr bool kGammaLate = V == 4 && (Q == kNormPlain || TPR == (Q == kNormFp8 ? 256 : 512));
   auto gamma16 = [&](int c) {
     return !a.gamma_f32 && c < nc ? static_cast<const uint4*>(a.gamma)[c] : make_uint4(0, 0, 0, 0);
   };
@@ -198,7 +200,8 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256) k_rmsnorm(const NormArg
     const float s = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
     if (row && sub == 0) a.scale[t] = s;
     // One division per row, and every quotient corrected by its remainder (row_quotient): dividing every value cost
-    // 69 against 50 us at 4096 x 7168; the correction costs 0.4 us there (46.2 -> 46.6). Scales outside the correction's range divide: below 2^-90, and infinite.
+    // 69 against 50 us at 4096 x 7168; the correction costs 0.4 us there (46.2 -> 46.6). Scales outside its range
+    // divide: below 2^-90, and infinite.
     const float inv = __fdiv_rn(1.0f, s);
     const bool divide = !(s >= 0x1p-90f && s <= 3.402823466e38f);
 #pragma unroll
