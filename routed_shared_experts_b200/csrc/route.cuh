@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
   const float NEG_INF = __int_as_float(0xff800000);
   const size_t row = static_cast<size_t>(t) * a.ld;
 
-  // every load of the row's inputs first: they are in flight together
+  // every load of the row's inputs first: they are in flight together (the bias moved down to its use: 4096 x 256 in
+  // groups 11.5 against 11.3 us)
   float l[VPL], bias[VPL];
   float mx = NEG_INF;
   bool on[VPL];
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
     const bool in = e < a.E;
     l[i] = in ? route_logit(a, row, e) : NEG_INF;
     on[i] = !(in && a.mask) || a.mask[e] != 0;
-    bias[i] = in && a.bias ? a.bias[e] : 0.f;
+    bias[i] = in && a.bias ? ld_global_here(a.bias + e) : 0.f;
   }
   const size_t out = static_cast<size_t>(t) * a.k + lane;
   if (a.num_valid && t >= *a.num_valid) {
