@@ -109,7 +109,8 @@ typedef int moe_status_t;
 
 /* Expert id of a padding row of a batch (moe_route): moe_align_sort drops its
  * slots without an error, moe_append_shared_slots gives the row no shared
- * slots, and stage 2 leaves the row of the output as it was. */
+ * slots, and stage 2 leaves the row of the output as it was. All ids of a row
+ * or none: stage 2 finishes a token when all of its slots have arrived. */
 #define MOE_NO_EXPERT INT32_MIN
 
 /* Activations of moe_linear. */
@@ -448,7 +449,8 @@ moe_status_t shared_expert_gate_dot(int dtype, const void* x, const void* w, int
  * epilogue:
  *     y[t,n] = act( (sum_k x[t,k] * w[n,k]) * x_scale[t] * w_scale[n] + bias[n] )
  *     out[t,n] = round( y[t,n] + residual[t,n] )
- * fp32 accumulation and epilogue, one rounding to the output type. Serves the
+ * fp32 accumulation and epilogue (the scales applied one after the other, in
+ * this order), one rounding to the output type. Serves the
  * attention output projection onto the residual stream, router logits in fp32
  * and dense feed-forward projections, from one token to a whole prefill.
  *   dtype      type of x and w: MOE_DT_BF16, MOE_DT_FP16 or MOE_DT_FP8_E4M3.
