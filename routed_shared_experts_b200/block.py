@@ -5,8 +5,9 @@
         --moe_linear(w_r)--> router logits (fp32) --> the layer
 
 ``MoEBlock`` owns the buffers between the steps and writes the layer's inputs
-(``x``, ``x_scale``, ``logits``, and ``x_r`` for the shared gate of an 8-bit layer) in place, so a step - captured or not - is three
-C-ABI calls more than the layer's own. The layer's output is added to the
+(``x``, ``x_scale``, ``logits``, and ``x_r`` for the shared gate of an 8-bit
+layer) in place, so a step - captured or not - is three C-ABI calls more than the
+layer's own. The layer's output is added to the
 residual stream by the next block's norm (``moe_rmsnorm_quantize`` takes the sum
 of its two inputs), not by a kernel of its own.
 """

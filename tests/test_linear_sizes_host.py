@@ -1,9 +1,6 @@
 """Arithmetic of moe_linear's kernels at the largest sizes it accepts, run on the
 host: the functions are those of the kernels' header."""
-import os
 import subprocess
-
-import pytest
 
 from routed_shared_experts_b200 import build
 
@@ -33,17 +30,20 @@ int main() { return check<2>() + check<4>() ? 1 : 0; }
 """
 
 
-def test_chunk_bytes_up_to_the_largest_rows(tmp_path):
-    """Bytes of a 64-byte chunk that a row of N values holds: T > 64 rows of 2^29
-    fp32 results (140 GB) fit a GPU, and their chunks are whole."""
-    src = tmp_path / "sizes.cu"
-    src.write_text(SRC)
-    exe = tmp_path / "sizes"
+def _run(tmp_path, source):
+    src, exe = tmp_path / "host.cu", tmp_path / "host"
+    src.write_text(source)
     cmd = [build._nvcc(), "-O1", "-std=c++17", *build.ARCH, "-cudart", "static", "-I", build.INCLUDE, "-I", build.CSRC,
            "-o", str(exe), str(src)]
     res = subprocess.run(cmd, capture_output=True, text=True)
     assert res.returncode == 0, res.stderr
-    run = subprocess.run([str(exe)], capture_output=True, text=True)
+    return subprocess.run([str(exe)], capture_output=True, text=True)
+
+
+def test_chunk_bytes_up_to_the_largest_rows(tmp_path):
+    """Bytes of a 64-byte chunk that a row of N values holds: T > 64 rows of 2^29
+    fp32 results (140 GB) fit a GPU, and their chunks are whole."""
+    run = _run(tmp_path, SRC)
     assert run.returncode == 0, run.stdout
 
 
@@ -78,11 +78,5 @@ int main() {
 def test_the_last_release_of_an_accumulator_is_waited_for(tmp_path):
     """The pair kernel's MMA thread ends with a wait for the release after each
     accumulator's last use: the wait must not pass on the release before it."""
-    src, exe = tmp_path / "tail.cu", tmp_path / "tail"
-    src.write_text(TAIL)
-    cmd = [build._nvcc(), "-O1", "-std=c++17", *build.ARCH, "-cudart", "static", "-I", build.INCLUDE, "-I", build.CSRC,
-           "-o", str(exe), str(src)]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    assert res.returncode == 0, res.stderr
-    run = subprocess.run([str(exe)], capture_output=True, text=True)
+    run = _run(tmp_path, TAIL)
     assert run.returncode == 0, run.stdout
